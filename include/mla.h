@@ -294,6 +294,42 @@ MLA_API int mla_sparse_fused_norm_rope_attn_rope_cast(
     void* workspace, size_t workspace_bytes, uint8_t* out_e4m3, float* out_scale, float* lse,
     void* stream);
 
+/* Appends tokens to a paged latent cache: RMSNorm of the compressed latent,
+ * rotation of its RoPE dims at the token's position, quantisation to the
+ * cache's row format and the write to the token's slot, in one launch
+ * [FlashMLA (AI Wiki), "The FP8 and FP4 KV cache", for the row formats].
+ *   kv            [n] rows of d bf16 values, kv_stride values apart (a
+ *                 multiple of 8; a column range of a wider matrix will do).
+ *                 d = 576 for 1152- and 656-byte rows, 512 for 528 and 288
+ *   slots         int32[n] physical slots (block * 64 + offset); a negative
+ *                 one marks a token without a slot (padding): its row is not
+ *                 read, nothing is written for it.  A slot >= num_slots is
+ *                 skipped too and sets the bad-index status.  The slots
+ *                 named must differ: which of two tokens with the same slot
+ *                 the row ends up with, or parts of both, is not defined
+ *   positions     int32[n] for the rotation, or NULL: the last 64 dims are
+ *                 stored as they are.  Pairs (2k, 2k+1) of them rotate by
+ *                 pos * rope_base^(-2k/64)
+ *   norm_gain     fp32[512] or NULL (no norm): dims 0..511 become
+ *                 x g / sqrt(mean(x^2) + eps).  The 512-dim latent includes
+ *                 its RoPE dims: they are normalised, then rotated
+ *   kcache        [num_slots] rows of row_bytes bytes, row_bytes one of
+ *     1152        576 bf16 (the dense cache)
+ *     656         per 128 dims scale = absmax/448 (fp32; 1 for a zero group)
+ *     528         per 32 dims scale = the least power of two >= absmax/448
+ *     288         per 16 dims scale = e4m3(absmax/6) (1 where that is 0)
+ *                 codes are value / scale rounded to the nearest, ties to
+ *                 even, saturating; bytes as the sparse decodes read them
+ *   rows          bf16 [n, d] or NULL: the rows as the cache stands for them,
+ *                 bf16(code * scale) (for a prefill over the same tokens);
+ *                 rows of tokens without a slot are left as they were
+ * Values are expected to be finite; a NaN or infinity stays in its own token's
+ * cache row (the norm and the scales of that row included). */
+MLA_API int mla_cache_append(const void* kv, int64_t kv_stride, int d, const int32_t* slots,
+                     const int32_t* positions, const float* norm_gain, float eps, float rope_base,
+                     int n, void* kcache, int64_t num_slots, int row_bytes, void* rows,
+                     void* stream);
+
 /* Dense decode without a caller workspace.  This entry point has no
  * counterpart in the method's published interface; it exists for callers
  * that cannot supply scratch memory at decode time (an embedder whose device

@@ -33,7 +33,7 @@ EXPORTED = [
     "mla_set_kernel_events", "mla_sparse_v41_workspace_size", "mla_sparse_decode_v41",
     "mla_sparse_decode_v41_fp4", "mla_sparse_fused_workspace_size",
     "mla_sparse_fused_norm_rope_attn_rope_cast", "mla_sparse_prefill_workspace_size",
-    "mla_sparse_prefill_fwd", "mla_set_slot_trace",
+    "mla_sparse_prefill_fwd", "mla_set_slot_trace", "mla_cache_append",
 ]
 
 
@@ -85,6 +85,8 @@ def lib():
                                              i32, vp, sz, vp, vp, vp]
         L.mla_sparse_fused_norm_rope_attn_rope_cast.argtypes = [
             vp, vp, f32, f32, vp, vp, i64, vp, i32, i32, i32, f32, i32, vp, sz, vp, vp, vp, vp]
+        L.mla_cache_append.argtypes = [vp, i64, i32, vp, vp, vp, f32, f32, i32, vp, i64, i32, vp,
+                                       vp]
         L.mla_device_status.argtypes = [ip, i32]
         L.mla_noalloc_scratch_bytes.argtypes = []
         L.mla_set_kernel_events.argtypes = [vp, vp]
@@ -110,6 +112,15 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
 
 
 def _require(cond, msg):
@@ -464,3 +475,62 @@ def mla_sparse_prefill_fwd(q, kv, indices, softmax_scale=None, d_v=512, topk_len
         int(d_v), float(softmax_scale), int(num_sm_parts), _ptr(ws), ws.numel(), _ptr(out),
         _ptr(lse), _stream(dev)))
     return out, lse
+
+
+# ------------------------------------------------------------------ cache writers
+
+def _int32(t, name, shape, device):
+    """`t` as a contiguous int32 tensor of `shape` on `device`."""
+    _require(tuple(t.shape) == tuple(shape), f"{name} must be {list(shape)}")
+    _require(t.device == device, f"{name} must be on {device}")
+    if t.dtype != torch.int32:
+        _require(t.dtype == torch.int64, f"{name} must be int32 (or int64)")
+        t = t.to(torch.int32)
+    return t.contiguous()
+
+
+def mla_cache_append(kv: torch.Tensor, slots: torch.Tensor, kcache: torch.Tensor,
+                     positions: Optional[torch.Tensor] = None,
+                     norm_gain: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     rope_base: float = 1e4, rows: Optional[torch.Tensor] = None):
+    """Append tokens to a paged latent cache: RMSNorm (with `norm_gain` [512]),
+    RoPE of the last 64 dims (with `positions` [n]), quantisation, scatter.
+    kv [n, 576] bf16 for a bf16 cache [NB, 64, 1, 576] or a 656-byte one (uint8
+    [..., 656]), [n, 512] for the 528- and 288-byte ones; its rows may be
+    strided.  slots [n] int32 physical slots (negative = padding, skipped; the
+    others must differ).  `rows` (bf16, kv's shape, contiguous) receives the
+    rows as the cache stands for them.  Writes into `kcache`; returns `rows`."""
+    if kcache.dtype == torch.bfloat16:
+        _require(kcache.shape[-1] == D_QK, "a bf16 kcache must be [..., 576]")
+        row_bytes = 2 * D_QK
+    else:
+        _require(kcache.dtype == torch.uint8 and kcache.shape[-1] in (656, 528, 288),
+                 "kcache must be bf16 [..., 576] or uint8 [..., 656], [..., 528] or [..., 288]")
+        row_bytes = int(kcache.shape[-1])
+    d = D_QK if row_bytes >= 656 else 512
+    _require(kv.is_cuda and kv.dim() == 2 and kv.shape[1] == d and kv.dtype == torch.bfloat16,
+             f"kv must be CUDA bf16 [n, {d}] for {row_bytes}-byte cache rows")
+    dev, n = kv.device, kv.shape[0]
+    _require(kcache.is_contiguous() and kcache.device == dev,
+             f"kcache must be contiguous and on {dev}")
+    if n == 0:
+        return rows
+    if kv.stride(1) != 1 or kv.stride(0) % 8 or (n > 1 and kv.stride(0) < d) or kv.data_ptr() % 16:
+        kv = kv.clone(memory_format=torch.contiguous_format)
+    slots = _int32(slots, "slots", (n,), dev)
+    if positions is not None:
+        positions = _int32(positions, "positions", (n,), dev)
+    if norm_gain is not None:
+        _require(tuple(norm_gain.shape) == (512,) and norm_gain.device == dev,
+                 f"norm_gain must be [512] on {dev}")
+        norm_gain = norm_gain.to(torch.float32).contiguous()
+    if rows is not None:
+        _require(tuple(rows.shape) == (n, d) and rows.dtype == torch.bfloat16 and
+                 rows.is_contiguous() and rows.device == dev,
+                 f"rows must be contiguous bf16 [{n}, {d}] on {dev}")
+    _call(dev, lib().mla_cache_append, kv.data_ptr(), max(kv.stride(0), d), d, slots.data_ptr(),
+          None if positions is None else positions.data_ptr(),
+          None if norm_gain is None else norm_gain.data_ptr(), eps, rope_base, n,
+          kcache.data_ptr(), kcache.numel() // kcache.shape[-1], row_bytes,
+          None if rows is None else rows.data_ptr())
+    return rows

@@ -1,0 +1,296 @@
+// append_kernel.cuh -- writes new tokens into a paged latent cache: RMSNorm of
+// the compressed latent, rotation of its RoPE dims at the token's position,
+// quantisation to the cache's row format, and the scatter to physical slots.
+// (The cache formats: [FlashMLA (AI Wiki), "The FP8 and FP4 KV cache"].)
+//
+// Per token with latent x (d = 576 for the bf16 and 656-byte rows, 512 for the
+// V4.1 rows) and physical slot s (block * 64 + offset, negative = no slot):
+//   y_i = x_i g_i / sqrt(mean_{j<512}(x_j^2) + eps)        (i < 512, optional)
+//   the last 64 dims rotated in pairs (2k, 2k + 1) by pos * base^(-2k/64)
+//                                                          (optional)
+//   1152 bytes  bf16(y)
+//    656 bytes  scale = absmax/448 per 128 dims (fp32, 1 for a zero group),
+//               codes e4m3(y / scale), the 64 RoPE dims in bf16
+//    528 bytes  scale = the least 2^e >= absmax/448 per 32 dims (E8M0)
+//    288 bytes  scale = e4m3(absmax/6) per 16 dims (1 where that is 0),
+//               codes e2m1(y / scale)
+// The V4.1 latent includes its RoPE dims, so its norm covers them and the
+// rotation follows the norm.  Optionally the rows are also written as the
+// cache stands for them: bf16(code * scale), what the attention kernels read.
+//
+// One warp per token: lane l holds the 16-byte units l and l + 32 (8 dims
+// each) of the first 512 dims, and lanes 0..7 the eight units behind them, so
+// that a quantisation group is 16, 4 or 2 neighbouring lanes of one unit index
+// and its maximum takes 4, 2 or 1 shuffles.  A warp keeps its gains in registers and
+// strides over the tokens.
+//
+// Precision: the norm's sum of squares is formed in fp64, and y in fp32 with
+// the exact products' low parts carried along (one rounding, as if y were
+// formed exactly), so that a code differs from the definition's only where y
+// lies within about 2^-24 of a rounding border.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "combine_kernel.cuh"
+#include "sparse_gather.cuh"
+
+namespace mla {
+
+constexpr int kRow1152 = 2 * kD;  // bf16 cache row
+constexpr int kAppendWarps = 8;
+constexpr int kAppendCtas = 4;  // CTAs per SM of a full grid
+
+struct AppendParams {
+  const __nv_bfloat16* kv;  // [n] rows of d values, kv_stride values apart
+  long long kv_stride;
+  const int32_t* slots;      // [n]
+  const int32_t* positions;  // [n], or null: no rotation
+  const float* gain;         // [512], or null: no norm
+  double eps;
+  double turns[kRope / 2];   // base^(-2k/64) / (2 pi), computed on the host in fp64
+  int n;
+  uint8_t* cache;  // [num_slots, row bytes]
+  long long num_slots;
+  __nv_bfloat16* rows;  // [n, d], or null
+};
+
+// x * g * inv with one rounding, inv = inv_hi + inv_lo: the product x g is
+// held exactly as hi + lo (Dekker's two-product by fma), and the low parts of
+// the second product are added before the result is rounded.
+__device__ __forceinline__ float mul3_once(float x, float g, float inv_hi, float inv_lo) {
+  const float hi = x * g;
+  const float lo = fmaf(x, g, -hi);
+  const float y = hi * inv_hi;
+  float e = fmaf(hi, inv_hi, -y);
+  e = fmaf(hi, inv_lo, e);
+  e = fmaf(lo, inv_hi, e);
+  return y + e;
+}
+
+// Eight fp32 values -> eight E2M1 codes (nearest, ties to even, saturating),
+// code 2i in the low nibble of byte i.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
+}
+
+// E2M1 code pair (low nibble first) -> two fp32 values (exact).  The byte is
+// cut out of the packed word by a shift and handed over in a 16-bit register:
+// unpacking a word that the same thread packed with mov.b32 {b0, b1, b2, b3}
+// (e2m1x8_to_f16x2 right behind cvt_e2m1x8) gave zeros for its upper two bytes.
+__device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b0, b1;\n\t"
+      "mov.b16 {b0, b1}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+      : "=r"(h)
+      : "h"(static_cast<uint16_t>(byte)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// E4M3 code pair -> two fp32 values (exact).
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t pair) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(pair)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// bf16(code * scale) of eight codes, each product rounded once.
+__device__ __forceinline__ uint4 scaled_bf16x8(const float* c, float scale) {
+  uint4 o;
+  o.x = ptx::pack_bf16x2(mul_round_odd(c[0], scale), mul_round_odd(c[1], scale));
+  o.y = ptx::pack_bf16x2(mul_round_odd(c[2], scale), mul_round_odd(c[3], scale));
+  o.z = ptx::pack_bf16x2(mul_round_odd(c[4], scale), mul_round_odd(c[5], scale));
+  o.w = ptx::pack_bf16x2(mul_round_odd(c[6], scale), mul_round_odd(c[7], scale));
+  return o;
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float* y) {
+  return make_uint4(ptx::pack_bf16x2(y[0], y[1]), ptx::pack_bf16x2(y[2], y[3]),
+                    ptx::pack_bf16x2(y[4], y[5]), ptx::pack_bf16x2(y[6], y[7]));
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 w, float* x) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(u[e] << 16);
+    x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+  }
+}
+
+// Rotates the unit's four pairs 4u .. 4u + 3; lane k holds pair k's cos, sin.
+// Every lane of the warp calls it (the shuffles); `mine` lanes take the result.
+__device__ __forceinline__ void rotate_unit(float* y, int u, bool mine, float cs, float sn) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float c = __shfl_sync(0xffffffffu, cs, (4 * u + e) & 31);
+    const float s = __shfl_sync(0xffffffffu, sn, (4 * u + e) & 31);
+    const float a = y[2 * e], b = y[2 * e + 1];
+    if (mine) {
+      y[2 * e] = a * c - b * s;
+      y[2 * e + 1] = a * s + b * c;
+    }
+  }
+}
+
+template <int kRowBytes>
+__global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const AppendParams P) {
+  static_assert(kRowBytes == kRow1152 || kRowBytes == kRow656 || kRowBytes == kRow528 ||
+                    kRowBytes == kRow288,
+                "1152-, 656-, 528- or 288-byte rows");
+  constexpr bool kWide = kRowBytes == kRow1152 || kRowBytes == kRow656;  // 576-dim latent
+  constexpr int kDim = kWide ? kD : kNope;
+  constexpr int kGroupLanes = kRowBytes == kRow656 ? 16 : kRowBytes == kRow528 ? 4 : 2;
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  float g[2][8];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[j][e] = P.gain ? __ldg(P.gain + (lane + 32 * j) * 8 + e) : 1.f;
+
+  for (long long t = (long long)blockIdx.x * kAppendWarps + warp; t < P.n;
+       t += (long long)gridDim.x * kAppendWarps) {
+    const int slot = P.slots[t];
+    if (slot < 0 || slot >= P.num_slots) {  // no slot: whatever the row holds is not read
+      if (slot >= 0 && lane == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x71);
+      continue;
+    }
+    const __nv_bfloat16* src = P.kv + t * P.kv_stride;
+    uint4 raw[3];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      raw[j] = *reinterpret_cast<const uint4*>(src + (lane + 32 * j) * 8);
+    raw[2] = make_uint4(0, 0, 0, 0);
+    if (kWide && lane < 8) raw[2] = *reinterpret_cast<const uint4*>(src + kNope + lane * 8);
+    float cs = 1.f, sn = 0.f;
+    if (P.positions) {
+      // the angle in turns, its whole turns dropped in fp64, the rest in fp32
+      const double a = static_cast<double>(P.positions[t]) * P.turns[lane];
+      sincospif(2.f * static_cast<float>(a - rint(a)), &sn, &cs);
+    }
+    float y[2][8], yr[8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) unpack_bf16x8(raw[j], y[j]);
+    unpack_bf16x8(raw[2], yr);
+
+    if (P.gain) {
+      double ss = 0.0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // the squares are exact in fp64
+          ss = fma(static_cast<double>(y[j][e]), static_cast<double>(y[j][e]), ss);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const double inv = 1.0 / sqrt(ss * (1.0 / kNope) + P.eps);
+      const float inv_hi = static_cast<float>(inv);
+      const float inv_lo = static_cast<float>(inv - static_cast<double>(inv_hi));
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[j][e] = mul3_once(y[j][e], g[j][e], inv_hi, inv_lo);
+    }
+    if (P.positions) {
+      if (kWide)
+        rotate_unit(yr, lane, lane < 8, cs, sn);  // dims 512..575
+      else
+        rotate_unit(y[1], lane - 24, lane >= 24, cs, sn);  // dims 448..511
+    }
+
+    uint8_t* row = P.cache + static_cast<size_t>(slot) * kRowBytes;
+    __nv_bfloat16* out = P.rows ? P.rows + t * kDim : nullptr;
+    if constexpr (kRowBytes == kRow1152) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint4 w = pack_bf16x8(y[j]);
+        *reinterpret_cast<uint4*>(row + (lane + 32 * j) * 16) = w;
+        if (out) *reinterpret_cast<uint4*>(out + (lane + 32 * j) * 8) = w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int u = lane + 32 * j;
+        const int group = u / kGroupLanes;
+        float amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[j][e]));
+#pragma unroll
+        for (int o = kGroupLanes / 2; o > 0; o >>= 1)
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        float c[8];
+        float scale;
+        if constexpr (kRowBytes == kRow528) {
+          // amax = m 2^e with 1 <= m < 2, 448 = 1.75 * 2^8: the least power of
+          // two >= amax/448 is 2^(e - 8), one more where m > 1.75
+          const uint32_t bits = __float_as_uint(amax);
+          int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+          e = amax > 0.f ? max(e, -127) : 0;  // at most 127 - 7 for a finite amax
+          scale = e8m0_to_float(static_cast<uint32_t>(e + 127));
+          const float up = ldexpf(1.f, -e);  // exact: y * 2^-e is y / scale
+#pragma unroll
+          for (int k = 0; k < 8; ++k) c[k] = y[j][k] * up;
+          if (lane % kGroupLanes == 0) row[kNope + group] = static_cast<uint8_t>(e + 127);
+        } else if constexpr (kRowBytes == kRow656) {
+          scale = amax > 0.f ? amax / 448.f : 1.f;
+          if (!(scale > 0.f)) scale = 1.f;  // absmax/448 below the least fp32 value
+#pragma unroll
+          for (int k = 0; k < 8; ++k) c[k] = y[j][k] / scale;
+          if (lane % kGroupLanes == 0)
+            *reinterpret_cast<float*>(row + kNope + 4 * group) = scale;
+        } else {
+          uint32_t code = cvt_e4m3x4(amax > 0.f ? amax / 6.f : 1.f, 0.f, 0.f, 0.f) & 0xFFu;
+          if (code == 0) code = 0x38;  // 1.0
+          scale = e4m3x2_to_float2(code).x;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) c[k] = y[j][k] / scale;
+          if (lane % kGroupLanes == 0) row[kNope / 2 + group] = static_cast<uint8_t>(code);
+        }
+        if constexpr (kRowBytes == kRow288) {
+          const uint32_t w = cvt_e2m1x8(c);
+          *reinterpret_cast<uint32_t*>(row + u * 4) = w;
+          if (out) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = e2m1x2_to_float2((w >> (8 * k)) & 0xFFu);
+              c[2 * k] = f.x;
+              c[2 * k + 1] = f.y;
+            }
+            *reinterpret_cast<uint4*>(out + u * 8) = scaled_bf16x8(c, scale);
+          }
+        } else {
+          const uint32_t lo = cvt_e4m3x4(c[0], c[1], c[2], c[3]);
+          const uint32_t hi = cvt_e4m3x4(c[4], c[5], c[6], c[7]);
+          *reinterpret_cast<uint2*>(row + u * 8) = make_uint2(lo, hi);
+          if (out) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = e4m3x2_to_float2((k < 2 ? lo : hi) >> (16 * (k & 1)));
+              c[2 * k] = f.x;
+              c[2 * k + 1] = f.y;
+            }
+            *reinterpret_cast<uint4*>(out + u * 8) = scaled_bf16x8(c, scale);
+          }
+        }
+      }
+    }
+    if (kWide && lane < 8) {
+      const uint4 w = pack_bf16x8(yr);
+      *reinterpret_cast<uint4*>(row + (kRowBytes == kRow1152 ? 2 * kNope : kNope + 16) +
+                                lane * 16) = w;
+      if (out) *reinterpret_cast<uint4*>(out + kNope + lane * 8) = w;
+    }
+  }
+}
+
+}  // namespace mla

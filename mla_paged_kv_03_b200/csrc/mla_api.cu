@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/mla.h"
+#include "append_kernel.cuh"
 #include "combine_kernel.cuh"
 #include "decode_kernel.cuh"
 #include "page_kernel.cuh"
@@ -1096,6 +1097,60 @@ int mla_sparse_decode_v41(const void* q, const uint8_t* kcache_528, int64_t num_
                             stream);
 }
 
+int mla_cache_append(const void* kv, int64_t kv_stride, int d, const int32_t* slots,
+                     const int32_t* positions, const float* norm_gain, float eps, float rope_base,
+                     int n, void* kcache, int64_t num_slots, int row_bytes, void* rows,
+                     void* stream) {
+  const bool wide = row_bytes == mla::kRow1152 || row_bytes == mla::kRow656;
+  MLA_CHECK_ARG(wide || row_bytes == mla::kRow528 || row_bytes == mla::kRow288,
+                "row_bytes must be 1152, 656, 528 or 288 (got %d)", row_bytes);
+  MLA_CHECK_ARG(d == (wide ? mla::kD : mla::kNope), "d must be %d for %d-byte rows (got %d)",
+                wide ? mla::kD : mla::kNope, row_bytes, d);
+  MLA_CHECK_ARG(n >= 0, "n must be >= 0 (got %d)", n);
+  MLA_CHECK_ARG(num_slots >= 1 && num_slots < (1LL << 31), "num_slots must be in [1, 2^31)");
+  MLA_CHECK_ARG(kv_stride >= d && kv_stride % 8 == 0 && kv_stride < (1LL << 32),
+                "kv_stride must be a multiple of 8 in [%d, 2^32) (got %lld)", d,
+                static_cast<long long>(kv_stride));
+  MLA_CHECK_ARG(std::isfinite(eps) && eps >= 0.f, "eps must be finite and >= 0");
+  MLA_CHECK_ARG(std::isfinite(rope_base) && rope_base > 0.f, "rope_base must be > 0");
+  MLA_CHECK_ARG(kv && slots && kcache, "null device pointer");
+  MLA_CHECK_ARG(aligned(kv, 16) && aligned(kcache, 16) && aligned(rows, 16),
+                "kv, kcache and rows must be 16-byte aligned");
+  MLA_CHECK_ARG(aligned(slots, 4) && aligned(positions, 4) && aligned(norm_gain, 4),
+                "slots, positions and norm_gain must be 4-byte aligned");
+  if (n == 0) return MLA_OK;
+  mla::AppendParams p{};
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.kv_stride = kv_stride;
+  p.slots = slots;
+  p.positions = positions;
+  p.gain = norm_gain;
+  p.eps = eps;
+  for (int k = 0; k < mla::kRope / 2; ++k)
+    p.turns[k] = std::pow(static_cast<double>(rope_base), -2.0 * k / mla::kRope) /
+                 6.283185307179586476925286766559;
+  p.n = n;
+  p.cache = static_cast<uint8_t*>(kcache);
+  p.num_slots = num_slots;
+  p.rows = static_cast<__nv_bfloat16*>(rows);
+  int dev = 0, sms = 0;
+  MLA_CUDA(cudaGetDevice(&dev));
+  MLA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  const int ctas = mla::ceil_div(n, mla::kAppendWarps);
+  const int grid = ctas < sms * mla::kAppendCtas ? ctas : sms * mla::kAppendCtas;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // ordinary launches: the kernel reads what earlier work of the stream wrote
+  if (row_bytes == mla::kRow1152)
+    mla::mla_append_kernel<mla::kRow1152><<<grid, 32 * mla::kAppendWarps, 0, st>>>(p);
+  else if (row_bytes == mla::kRow656)
+    mla::mla_append_kernel<mla::kRow656><<<grid, 32 * mla::kAppendWarps, 0, st>>>(p);
+  else if (row_bytes == mla::kRow528)
+    mla::mla_append_kernel<mla::kRow528><<<grid, 32 * mla::kAppendWarps, 0, st>>>(p);
+  else
+    mla::mla_append_kernel<mla::kRow288><<<grid, 32 * mla::kAppendWarps, 0, st>>>(p);
+  MLA_CUDA(cudaGetLastError());
+  return MLA_OK;
+}
 
 int mla_set_slot_trace(int32_t* trace, int64_t capacity) {
   MLA_CHECK_ARG(!trace || capacity >= 0, "capacity must be >= 0");
