@@ -294,6 +294,51 @@ MLA_API int mla_sparse_fused_norm_rope_attn_rope_cast(
     void* workspace, size_t workspace_bytes, uint8_t* out_e4m3, float* out_scale, float* lse,
     void* stream);
 
+/* Dense decode of a batch whose sequences share a long prefix (a system
+ * prompt, a document): sequence b's tokens are the prefix_len tokens of
+ * prefix_table, then the cache_seqlens[b] tokens of its block_table row.  The
+ * result is that of mla_decode_fwd over the joined sequence, but the prefix is
+ * read once for groups of 128 query rows of any sequences instead of once per
+ * sequence.
+ *   prefix_table  int32[ceil(prefix_len / 64)] blocks of the prefix (may be
+ *                 NULL when prefix_len is 0; a partial last page is fine)
+ *   prefix_len    tokens of the prefix, >= 0 (host value, part of the plan)
+ *   block_table, max_pages, cache_seqlens: each sequence's own tokens (0 of
+ *                 them is allowed), as in mla_decode_fwd
+ *   d_v           512
+ *   causal        nonzero: query i of s_q sees prefix_len + L - s_q + 1 + i
+ *                 tokens (bottom-right alignment over the joined sequence)
+ *   metadata, num_splits, num_sm_parts: from mla_shared_prefix_get_metadata
+ *                 for the same cache_seqlens, rows_per_kv = s_q * h_q and
+ *                 prefix_len; num_sm_parts from mla_num_sm_parts(device, 128,
+ *                 1).  Sizes from mla_shared_prefix_metadata_size.  A plan of
+ *                 another batch, row count or prefix presence is not run: it
+ *                 sets the bad-index status and leaves out and lse as they
+ *                 were
+ *   workspace     >= mla_shared_prefix_workspace_size() bytes, 16-byte aligned
+ * At most 8192 groups of 128 query rows (over the prefix plus over own
+ * tokens).  Other arguments, ownership and errors as in mla_decode_fwd; a
+ * row that sees nothing gives O = 0 and LSE = -inf.  Two launches on `stream`
+ * (attention, merge) after the planner's one. */
+MLA_API int mla_shared_prefix_metadata_size(int batch, int rows_per_kv, int prefix_len,
+                                            int num_sm_parts, size_t* metadata_bytes,
+                                            size_t* num_splits_bytes);
+MLA_API int mla_shared_prefix_get_metadata(const int32_t* cache_seqlens, int batch,
+                                           int rows_per_kv, int h_kv, int prefix_len,
+                                           int num_sm_parts, int32_t* metadata,
+                                           int32_t* num_splits, void* stream);
+MLA_API int mla_shared_prefix_workspace_size(int batch, int rows_per_kv, int prefix_len,
+                                             int num_sm_parts, size_t* bytes);
+MLA_API int mla_shared_prefix_decode_fwd(const void* q, const void* kcache, int num_blocks,
+                                         const int32_t* prefix_table, int prefix_len,
+                                         const int32_t* block_table, int max_pages,
+                                         const int32_t* cache_seqlens, int batch, int s_q, int h_q,
+                                         int h_kv, int d_v, float softmax_scale, int causal,
+                                         const int32_t* metadata, const int32_t* num_splits,
+                                         int num_sm_parts, void* workspace,
+                                         size_t workspace_bytes, void* out, float* lse,
+                                         void* stream);
+
 /* Appends tokens to a paged latent cache: RMSNorm of the compressed latent,
  * rotation of its RoPE dims at the token's position, quantisation to the
  * cache's row format and the write to the token's slot, in one launch
@@ -383,6 +428,9 @@ MLA_API int mla_set_kernel_events(void* start_event, void* stop_event);
  *                 rows read as V.  Only tokens of pages that hold part of the
  *                 sequence are written (a partial last page in full); an
  *                 out-of-range block id shows as block 0.
+ *               shared-prefix decode: N = (ceil(prefix_len / 64) + batch *
+ *                 max_pages) * 64: the prefix's tokens, then the sequences'
+ *                 own ones laid out as in dense decode
  *               sparse decode and fused sparse decode: N = batch * s_q *
  *                 topk; entry p * topk + j holds the slot entry j of query p
  *                 read (-1 if unused or out of range) in plane 0, and the row

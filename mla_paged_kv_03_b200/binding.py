@@ -34,6 +34,8 @@ EXPORTED = [
     "mla_sparse_decode_v41_fp4", "mla_sparse_fused_workspace_size",
     "mla_sparse_fused_norm_rope_attn_rope_cast", "mla_sparse_prefill_workspace_size",
     "mla_sparse_prefill_fwd", "mla_set_slot_trace", "mla_cache_append",
+    "mla_shared_prefix_metadata_size", "mla_shared_prefix_get_metadata",
+    "mla_shared_prefix_workspace_size", "mla_shared_prefix_decode_fwd",
 ]
 
 
@@ -87,6 +89,12 @@ def lib():
             vp, vp, f32, f32, vp, vp, i64, vp, i32, i32, i32, f32, i32, vp, sz, vp, vp, vp, vp]
         L.mla_cache_append.argtypes = [vp, i64, i32, vp, vp, vp, f32, f32, i32, vp, i64, i32, vp,
                                        vp]
+        L.mla_shared_prefix_metadata_size.argtypes = [i32, i32, i32, i32, szp, szp]
+        L.mla_shared_prefix_get_metadata.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp]
+        L.mla_shared_prefix_workspace_size.argtypes = [i32, i32, i32, i32, szp]
+        L.mla_shared_prefix_decode_fwd.argtypes = [
+            vp, vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32, f32, i32, vp, vp, i32, vp,
+            sz, vp, vp, vp]
         L.mla_device_status.argtypes = [ip, i32]
         L.mla_noalloc_scratch_bytes.argtypes = []
         L.mla_set_kernel_events.argtypes = [vp, vp]
@@ -474,6 +482,86 @@ def mla_sparse_prefill_fwd(q, kv, indices, softmax_scale=None, d_v=512, topk_len
         _ptr(q), _ptr(kv), kv.numel() // D_QK, _ptr(idx), topk, _ptr(tl), _ptr(sk), s_q, h_q,
         int(d_v), float(softmax_scale), int(num_sm_parts), _ptr(ws), ws.numel(), _ptr(out),
         _ptr(lse), _stream(dev)))
+    return out, lse
+
+
+# ------------------------------------------------------------------ shared prefix
+
+def mla_shared_prefix_workspace_size(batch, rows_per_kv, prefix_len, num_sm_parts) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().mla_shared_prefix_workspace_size(int(batch), int(rows_per_kv), int(prefix_len),
+                                                  int(num_sm_parts), ctypes.byref(out)))
+    return out.value
+
+
+def mla_shared_prefix_get_metadata(cache_seqlens: torch.Tensor, prefix_len: int,
+                                   rows_per_kv: int, h_kv: int = 1,
+                                   num_sm_parts: Optional[int] = None):
+    """Plan of a shared-prefix decode on the current stream: (metadata,
+    num_splits, num_sm_parts), for the sequences' own lengths `cache_seqlens`
+    [b] int32 and rows_per_kv = s_q * h_q; the layers of a step share it."""
+    _require(cache_seqlens.is_cuda and cache_seqlens.dtype == torch.int32,
+             "cache_seqlens must be a CUDA int32 tensor")
+    sl = cache_seqlens.contiguous()
+    if num_sm_parts is None:
+        num_sm_parts = mla_num_sm_parts(128, h_kv, sl.device)
+    m, n = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().mla_shared_prefix_metadata_size(sl.numel(), int(rows_per_kv), int(prefix_len),
+                                                 int(num_sm_parts), ctypes.byref(m),
+                                                 ctypes.byref(n)))
+    meta = torch.empty((num_sm_parts, 8), dtype=torch.int32, device=sl.device)
+    splits = torch.empty((n.value // 4,), dtype=torch.int32, device=sl.device)
+    _call(sl.device, lib().mla_shared_prefix_get_metadata, sl.data_ptr(), sl.numel(),
+          int(rows_per_kv), int(h_kv), int(prefix_len), int(num_sm_parts), meta.data_ptr(),
+          splits.data_ptr())
+    return meta, splits, num_sm_parts
+
+
+def mla_shared_prefix_decode_fwd(q: torch.Tensor, kcache: torch.Tensor,
+                                 prefix_table: Optional[torch.Tensor], prefix_len: int,
+                                 block_table: torch.Tensor, cache_seqlens: torch.Tensor,
+                                 metadata: torch.Tensor, num_splits: torch.Tensor,
+                                 num_sm_parts: int, causal: bool = True,
+                                 softmax_scale: Optional[float] = None, out=None, lse=None,
+                                 workspace=None):
+    """Dense decode of a batch that shares a prefix.  q [b, s_q, h_q, 576] bf16,
+    kcache [NB, 64, 1, 576] bf16; prefix_table [>= ceil(prefix_len/64)] int32
+    blocks of the prefix; block_table [b, max_pages] and cache_seqlens [b] int32
+    the sequences' own tokens behind it.  Returns (out [b, s_q, h_q, 512] bf16,
+    lse [b, s_q, h_q] fp32)."""
+    _require(q.is_cuda and q.dim() == 4 and q.shape[-1] == D_QK and q.dtype == torch.bfloat16,
+             "q must be CUDA bf16 [b, s_q, h_q, 576]")
+    _require(kcache.dim() == 4 and kcache.shape[1] == 64 and kcache.shape[-1] == D_QK and
+             kcache.dtype == torch.bfloat16 and kcache.is_contiguous(),
+             "kcache must be contiguous [NB, 64, h_kv, 576] bf16")
+    b, s_q, h_q, _ = q.shape
+    dev = q.device
+    _require(block_table.dim() == 2, "block_table must be [b, max_pages]")
+    bt = _int32(block_table, "block_table", (b, block_table.shape[1]), dev)
+    sl = _int32(cache_seqlens, "cache_seqlens", (b,), dev)
+    pt = None
+    if prefix_len > 0:
+        _require(prefix_table is not None and prefix_table.dim() == 1 and
+                 prefix_table.numel() >= -(-prefix_len // 64),
+                 "prefix_table must be [>= ceil(prefix_len / 64)]")
+        pt = _int32(prefix_table, "prefix_table", prefix_table.shape, dev)
+    _require(metadata.numel() >= 8 * num_sm_parts and metadata.dtype == torch.int32 and
+             num_splits.dtype == torch.int32 and metadata.device == dev and
+             num_splits.device == dev, f"metadata and num_splits must be the plan, on {dev}")
+    q = q.contiguous()
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D_QK)
+    if out is None:
+        out = torch.empty((b, s_q, h_q, 512), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((b, s_q, h_q), dtype=torch.float32, device=dev)
+    ws = _workspace(mla_shared_prefix_workspace_size(b, s_q * h_q, prefix_len, num_sm_parts), dev,
+                    workspace)
+    _call(dev, lib().mla_shared_prefix_decode_fwd, q.data_ptr(), kcache.data_ptr(),
+          kcache.shape[0], None if pt is None else pt.data_ptr(), prefix_len, bt.data_ptr(),
+          bt.shape[1], sl.data_ptr(), b, s_q, h_q, kcache.shape[2], 512, softmax_scale,
+          int(causal), metadata.data_ptr(), num_splits.data_ptr(), num_sm_parts, ws.data_ptr(),
+          ws.numel() * ws.element_size(), out.data_ptr(), lse.data_ptr())
     return out, lse
 
 

@@ -274,7 +274,9 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* total) {
 
 // Split-KV planner of one CTA: the closed forms of mla_common.h evaluated in
 // parallel (prefix sums by block scans, one metadata row per thread).
-__device__ void plan_block(const int32_t* seqlens, int batch, int num_parts, const PlanParams pp,
+// seqlens(b): the length of sequence (or unit) b.
+template <class Lengths>
+__device__ void plan_block(const Lengths seqlens, int batch, int num_parts, const PlanParams pp,
                            int32_t* metadata, int32_t* num_splits, int32_t* ws_base,
                            int32_t* split_list, int list_cap) {
   const int o = pp.o, g = pp.g;
@@ -284,7 +286,7 @@ __device__ void plan_block(const int32_t* seqlens, int batch, int num_parts, con
   int carry = 0;
   for (int base = 0; base < batch; base += kPlanThreads) {
     const int b = base + tid;
-    const int L = b < batch ? seqlens[b] : 0;
+    const int L = b < batch ? seqlens(b) : 0;
     const int v = b < batch ? o + u * granules_of(L, g) : 0;
     int chunk_total;
     const int ex = block_exclusive_scan(v, &chunk_total);
@@ -344,7 +346,108 @@ __global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const int32_t* s
                                                                int32_t* split_list, int list_cap) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();  // the decode grid waits for this one at its start
-  plan_block(seqlens, batch, num_parts, pp, metadata, num_splits, ws_base, split_list, list_cap);
+  plan_block([=](int b) { return seqlens[b]; }, batch, num_parts, pp, metadata, num_splits,
+             ws_base, split_list, list_cap);
+}
+
+// Units of a shared-prefix decode: n_prefix of prefix_len tokens, then
+// own_groups for each sequence's own tokens.  Entry 5 of each metadata row
+// holds the unit count, by which the decode recognises its plan.
+__global__ void __launch_bounds__(kPlanThreads)
+    mla_shared_plan_kernel(const int32_t* seqlens, int units, int n_prefix, int prefix_len,
+                           int own_groups, int num_parts, const PlanParams pp, int32_t* metadata,
+                           int32_t* num_splits) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  plan_block(
+      [=](int u) { return u < n_prefix ? prefix_len : seqlens[(u - n_prefix) / own_groups]; },
+      units, num_parts, pp, metadata, num_splits, nullptr, nullptr, 0);
+  __syncthreads();
+  for (int p = threadIdx.x; p < num_parts; p += kPlanThreads) metadata[p * kMetaInts + 5] = units;
+}
+
+// Merge of a shared-prefix decode: a query row's partials are those of its
+// prefix unit and those of its sequence's own-token unit.
+struct SharedCombineParams {
+  int units, n_prefix, own_groups, R, total_rows;
+  const int32_t* metadata;    // entry 5: the plan's unit count
+  const int32_t* num_splits;  // [units + 1]
+  const float* ws_o;          // [splits, 128, 512]
+  const float* ws_lse;        // [splits, 128]
+  __nv_bfloat16* out;         // [total_rows, 512]
+  float* lse;                 // [total_rows]
+};
+
+// One warp per row, or (kRowPerCta, few rows) a CTA per row whose warps take
+// every kCombineWarps-th partial.  Lane l owns float4 groups l, l + 32, ...
+template <bool kRowPerCta>
+__global__ void __launch_bounds__(kCombineThreads)
+    mla_shared_combine_kernel(const SharedCombineParams P) {
+  __shared__ float4 s_acc[kRowPerCta ? kCombineWarps - 1 : 1][kNope / 4];
+  ptx::grid_dep_wait();  // the attention kernel's partials are complete
+  if (P.metadata[5] != P.units) return;  // not this decode's plan: the attention kernel said so
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = kRowPerCta ? blockIdx.x : blockIdx.x * kCombineWarps + warp;
+  if (row >= P.total_rows) return;
+  const int b = row / P.R, r = row - b * P.R;
+  const int u0 = P.n_prefix ? row >> 7 : 0;
+  const int u1 = P.n_prefix + b * P.own_groups + (r >> 7);
+  const int n0 = P.n_prefix ? P.num_splits[u0 + 1] - P.num_splits[u0] : 0;
+  const int n = n0 + P.num_splits[u1 + 1] - P.num_splits[u1];
+  const size_t base0 = P.n_prefix ? (size_t)P.num_splits[u0] * 128 + (row & 127) : 0;
+  const size_t base1 = (size_t)P.num_splits[u1] * 128 + (r & 127);
+  auto at = [&](int i) -> size_t {  // workspace row of partial i
+    return i < n0 ? base0 + (size_t)i * 128 : base1 + (size_t)(i - n0) * 128;
+  };
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, P.ws_lse[at(i)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float sum = 0.f;
+  if (m != -INFINITY)
+    for (int i = lane; i < n; i += 32) sum += expf(P.ws_lse[at(i)] - m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float lse = m == -INFINITY ? -INFINITY : m + logf(sum);
+
+  float4 acc[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int k0 = kRowPerCta ? warp : 0;
+  constexpr int kStep = kRowPerCta ? kCombineWarps : 1;
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    float wl = 0.f;
+    if (c0 + lane < n) {
+      const float li = P.ws_lse[at(c0 + lane)];
+      wl = lse == -INFINITY || li == -INFINITY ? 0.f : expf(li - lse);
+    }
+    const int cn = min(32, n - c0);
+    for (int k = k0; k < cn; k += kStep) {
+      const float w = __shfl_sync(0xffffffffu, wl, k);
+      const float4* src = reinterpret_cast<const float4*>(P.ws_o + at(c0 + k) * kNope);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fma_acc(acc[j], w, src[lane + 32 * j]);
+    }
+  }
+  if constexpr (kRowPerCta) {
+    if (warp > 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s_acc[warp - 1][lane + 32 * j] = acc[j];
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      for (int w = 0; w < kCombineWarps - 1; ++w) fma_acc(acc[j], 1.f, s_acc[w][lane + 32 * j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint2 pk;
+    pk.x = ptx::pack_bf16x2(acc[j].x, acc[j].y);
+    pk.y = ptx::pack_bf16x2(acc[j].z, acc[j].w);
+    *reinterpret_cast<uint2*>(P.out + (size_t)row * kNope + 4 * (lane + 32 * j)) = pk;
+  }
+  if (lane == 0) P.lse[row] = lse;
 }
 
 }  // namespace mla

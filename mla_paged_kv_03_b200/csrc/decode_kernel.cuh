@@ -46,7 +46,7 @@
 
 namespace mla {
 
-enum Mode : int { kDense = 0, kFused = 1 };
+enum Mode : int { kDense = 0, kFused = 1, kSharedPrefix = 2 };
 
 struct DecodeParams {
   int batch;       // sequences
@@ -90,6 +90,16 @@ struct DecodeParams {
   // as 9) or 8 (a 512-dim latent: q is [rows, 512], and the cache's dims
   // 512..575 are not read)
   int qk_chunks;
+  // shared prefix (CTA-pair kernel): the units are first the n_prefix groups
+  // of 128 of all batch * R query rows over the prefix, then, per sequence,
+  // own_groups groups of 128 of its rows over its own tokens (block_table,
+  // seqlens); partials of unit u are rows (num_splits[u] + split) * 128 ..
+  int n_prefix;
+  int own_groups;
+  int total_rows;               // query rows of all sequences
+  int prefix_len;               // tokens of the prefix
+  int prefix_pages;             // ceil(prefix_len / 64)
+  const int32_t* prefix_table;  // [prefix_pages]
 };
 
 namespace cfg {
@@ -161,7 +171,7 @@ struct __align__(8) Ctrl {
 static_assert(sizeof(Ctrl) <= cfg::kMiscBytes, "control block too large");
 
 struct Unit {
-  int b, lo, hi, split, nsplit;
+  int b, lo, hi, split, nsplit;  // shared prefix: b is the unit, not a sequence
   int L;      // tokens attended: cache_seqlens[b], at most max_pages * 64
   int L_raw;  // cache_seqlens[b] as given (the planner counted its tiles)
 };
@@ -180,7 +190,14 @@ struct UnitIter {
   __device__ bool next(const DecodeParams& P, Unit& u) {
     while (b <= b_end) {
       const int bb = b++;
-      const int L_raw = P.seqlens[bb];
+      bool prefix = false;
+      int L_raw;
+      if constexpr (kMode == kSharedPrefix) {
+        prefix = bb < P.n_prefix;
+        L_raw = prefix ? P.prefix_len : P.seqlens[(bb - P.n_prefix) / P.own_groups];
+      } else {
+        L_raw = P.seqlens[bb];
+      }
       const int lo = (bb == b_first) ? t_begin : 0;
       const int tiles = tiles_of(L_raw);  // the planner's tiles
       const int hi = (bb == b_end) ? min(t_end, tiles) : tiles;
@@ -196,7 +213,7 @@ struct UnitIter {
       // input fault; tiles past it are fully masked, so every split the
       // planner counted still writes its (empty) partial.
       u.L = L_raw;
-      if (L_raw > P.max_pages * kPage) {
+      if (!prefix && L_raw > P.max_pages * kPage) {
         ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x30);
         u.L = P.max_pages * kPage;
       }
@@ -249,8 +266,8 @@ __device__ __forceinline__ float ex2(float x) {
 // offset) of the 64 tokens of page `page` of sequence b, in plane 0 (bit 0
 // of `planes`) and / or plane 1 (bit 1).
 __device__ __forceinline__ void trace_page(const DecodeParams& P, int b, int page, int blk,
-                                           int planes) {
-  int32_t* t = P.trace + (size_t)b * P.max_pages * kPage + (size_t)page * kPage;
+                                           int planes, size_t first = 0) {
+  int32_t* t = P.trace + first + (size_t)b * P.max_pages * kPage + (size_t)page * kPage;
   for (int i = threadIdx.x & 31; i < kPage; i += 32) {
     if (planes & 1) t[i] = blk * kPage + i;
     if (planes & 2) t[P.trace_plane + i] = blk * kPage + i;

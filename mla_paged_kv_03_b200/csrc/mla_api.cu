@@ -327,14 +327,14 @@ int launch_page_decode(const void* q, const CUtensorMap& tkv, const mla::DecodeP
 // 2-CTA kernel for more than 64 query rows per KV head: clusters of two CTAs,
 // one pair per scheduler part and 128-row group.
 // In gather mode tkv is the gather map of the row array and no V map is used.
-template <bool kGather>
+template <bool kGather, bool kShared = false>
 int launch_pair_decode(const void* q, const void* kcache, const CUtensorMap& tkv,
                        const mla::DecodeParams& p, cudaStream_t st) {
   CUtensorMap tq3, tv3;
   // q is [rows, 64 * qk_chunks] (576 wide, or 512 for a 512-dim latent)
   const int qk = p.qk_chunks ? p.qk_chunks : mla::kNumChunks;
-  int rc = make_latent_map3(&tq3, q, static_cast<long long>(p.batch) * p.R, qk, 64,
-                            qk * mla::kChunkD);
+  const long long q_rows = kShared ? p.total_rows : static_cast<long long>(p.batch) * p.R;
+  int rc = make_latent_map3(&tq3, q, q_rows, qk, 64, qk * mla::kChunkD);
   if (rc != MLA_OK) return rc;
   if (kGather)
     tv3 = tkv;
@@ -344,7 +344,7 @@ int launch_pair_decode(const void* q, const void* kcache, const CUtensorMap& tkv
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(mla::mla_pair_decode_kernel<kGather>,
+    attr_err = cudaFuncSetAttribute(mla::mla_pair_decode_kernel<kGather, kShared>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     mla::pcfg::kSmemBytes);
   });
@@ -353,7 +353,8 @@ int launch_pair_decode(const void* q, const void* kcache, const CUtensorMap& tkv
   PdlLaunch L(dim3(static_cast<unsigned>(2 * p.num_parts * p.n_groups)), dim3(mla::pcfg::kThreads),
               mla::pcfg::kSmemBytes, st, 2);
   if ((rc = record_start(st)) != MLA_OK) return rc;
-  MLA_CUDA(cudaLaunchKernelEx(&L.cfg, mla::mla_pair_decode_kernel<kGather>, tq3, tkv, tv3, p));
+  MLA_CUDA(cudaLaunchKernelEx(&L.cfg, mla::mla_pair_decode_kernel<kGather, kShared>, tq3, tkv, tv3,
+                              p));
   return record_stop(st);
 }
 
@@ -576,6 +577,31 @@ int prefill_parts(int num_sm_parts, int h_q, int* parts) {
   const int cap = sms / (2 * groups);
   *parts = num_sm_parts < cap ? num_sm_parts : cap;
   if (*parts < 1) *parts = 1;
+  return MLA_OK;
+}
+
+// Units of a shared-prefix decode: groups of 128 query rows over the prefix,
+// then per sequence groups of 128 of its rows over its own tokens.
+struct SharedUnits {
+  int n_prefix, own_groups, units;
+};
+
+int shared_units(int batch, int rows_per_kv, int prefix_len, SharedUnits* su) {
+  MLA_CHECK_ARG(batch >= 0 && rows_per_kv >= 1, "batch >= 0 and rows_per_kv >= 1 required");
+  MLA_CHECK_ARG(prefix_len >= 0, "prefix_len must be >= 0 (got %d)", prefix_len);
+  const long long rows = static_cast<long long>(batch) * rows_per_kv;
+  const long long groups = mla::ceil_div(rows_per_kv, 128);
+  const long long n_prefix = prefix_len > 0 ? (rows + 127) / 128 : 0;
+  MLA_CHECK_ARG(n_prefix + batch * groups <= mla::kPlanMaxBatch,
+                "at most %d row groups of 128 (got %lld over the prefix, %lld over own tokens)",
+                mla::kPlanMaxBatch, n_prefix, batch * groups);
+  const long long cost =
+      n_prefix * (mla::kPlanOverheadPair +
+                  2LL * mla::kPlanTileCost * mla::granules_of(prefix_len, 2));
+  MLA_CHECK_ARG(cost <= mla::kPlanMaxTotal / 2, "rows * prefix_len too large for the planner");
+  su->n_prefix = static_cast<int>(n_prefix);
+  su->own_groups = static_cast<int>(groups);
+  su->units = static_cast<int>(n_prefix + batch * groups);
   return MLA_OK;
 }
 
@@ -1095,6 +1121,139 @@ int mla_sparse_decode_v41(const void* q, const uint8_t* kcache_528, int64_t num_
   return sparse_decode_impl(mla::kRow528, q, kcache_528, num_slots, indices, topk, batch, s_q, h_q,
                             512, softmax_scale, num_sm_parts, workspace, workspace_bytes, out, lse,
                             stream);
+}
+
+int mla_shared_prefix_metadata_size(int batch, int rows_per_kv, int prefix_len, int num_sm_parts,
+                                    size_t* metadata_bytes, size_t* num_splits_bytes) {
+  SharedUnits su;
+  int rc = shared_units(batch, rows_per_kv, prefix_len, &su);
+  if (rc != MLA_OK) return rc;
+  return mla_metadata_size(su.units, num_sm_parts, metadata_bytes, num_splits_bytes);
+}
+
+int mla_shared_prefix_workspace_size(int batch, int rows_per_kv, int prefix_len, int num_sm_parts,
+                                     size_t* bytes) {
+  SharedUnits su;
+  int rc = shared_units(batch, rows_per_kv, prefix_len, &su);
+  if (rc != MLA_OK) return rc;
+  return mla_workspace_size(su.units, 128, mla::kNope, num_sm_parts, bytes);
+}
+
+int mla_shared_prefix_get_metadata(const int32_t* cache_seqlens, int batch, int rows_per_kv,
+                                   int h_kv, int prefix_len, int num_sm_parts, int32_t* metadata,
+                                   int32_t* num_splits, void* stream) {
+  if (h_kv != 1) return fail(MLA_ERR_UNSUPPORTED, "h_kv must be 1 (got %d)", h_kv);
+  SharedUnits su;
+  int rc = shared_units(batch, rows_per_kv, prefix_len, &su);
+  if (rc != MLA_OK) return rc;
+  MLA_CHECK_ARG(num_sm_parts >= 1 && num_sm_parts <= mla::kCombineMaxSplits,
+                "num_sm_parts must be in [1, %d] (got %d)", mla::kCombineMaxSplits, num_sm_parts);
+  MLA_CHECK_ARG(metadata && num_splits && (cache_seqlens || batch == 0), "null device pointer");
+  MLA_CHECK_ARG(aligned(cache_seqlens, 4) && aligned(metadata, 4) && aligned(num_splits, 4),
+                "int32 arrays must be 4-byte aligned");
+  mla::mla_shared_plan_kernel<<<1, mla::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      cache_seqlens, su.units, su.n_prefix, prefix_len, su.own_groups, num_sm_parts,
+      mla::plan_params(128), metadata, num_splits);
+  MLA_CUDA(cudaGetLastError());
+  return MLA_OK;
+}
+
+int mla_shared_prefix_decode_fwd(const void* q, const void* kcache, int num_blocks,
+                                 const int32_t* prefix_table, int prefix_len,
+                                 const int32_t* block_table, int max_pages,
+                                 const int32_t* cache_seqlens, int batch, int s_q, int h_q,
+                                 int h_kv, int d_v, float softmax_scale, int causal,
+                                 const int32_t* metadata, const int32_t* num_splits,
+                                 int num_sm_parts, void* workspace, size_t workspace_bytes,
+                                 void* out, float* lse, void* stream) {
+  if (h_kv != 1) return fail(MLA_ERR_UNSUPPORTED, "h_kv must be 1 (got %d)", h_kv);
+  if (d_v != mla::kNope)
+    return fail(MLA_ERR_UNSUPPORTED, "the shared-prefix decode has d_v = 512 (got %d)", d_v);
+  MLA_CHECK_ARG(s_q >= 1, "s_q must be >= 1 (got %d)", s_q);
+  int rc = check_common_dense(q, kcache, block_table, max_pages, num_blocks, cache_seqlens, batch,
+                              h_q, softmax_scale, metadata, num_splits, num_sm_parts, workspace);
+  if (rc != MLA_OK) return rc;
+  MLA_CHECK_ARG(out && lse, "null output pointer");
+  MLA_CHECK_ARG(aligned(out, 16) && aligned(lse, 4), "out must be 16-byte aligned, lse 4-byte");
+  MLA_CHECK_ARG(static_cast<long long>(s_q) * h_q * (batch > 0 ? batch : 1) < (1LL << 31) - 128,
+                "batch * s_q * h_q must fit in int32");
+  SharedUnits su;
+  if ((rc = shared_units(batch, s_q * h_q, prefix_len, &su)) != MLA_OK) return rc;
+  MLA_CHECK_ARG(prefix_len == 0 || (prefix_table && aligned(prefix_table, 4)),
+                "prefix_table is null or misaligned");
+  MLA_CHECK_ARG(static_cast<long long>(prefix_len) + static_cast<long long>(max_pages) * mla::kPage <
+                    (1LL << 31) - 128,
+                "prefix_len + max_pages * 64 must fit in int32");
+  const WsLayout w = dense_ws_layout(su.units, 128, mla::kNope, num_sm_parts);
+  MLA_CHECK_ARG(workspace_bytes >= w.total, "workspace too small: %zu < %zu", workspace_bytes,
+                w.total);
+  const int prefix_pages = mla::ceil_div(prefix_len, mla::kPage);
+  const long long trace_plane =
+      (static_cast<long long>(prefix_pages) + static_cast<long long>(batch) * max_pages) *
+      mla::kPage;
+  if ((rc = check_trace(trace_plane)) != MLA_OK) return rc;
+  if (batch == 0) return MLA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  CUtensorMap tkv;
+  if ((rc = make_latent_map(&tkv, kcache, static_cast<long long>(num_blocks) * mla::kPage)) !=
+      MLA_OK)
+    return rc;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  mla::DecodeParams p{};
+  p.batch = su.units;
+  p.s_q = s_q;
+  p.h_q = h_q;
+  p.R = s_q * h_q;
+  p.d_v = d_v;
+  p.n_groups = 1;
+  p.num_parts = num_sm_parts;
+  p.num_blocks = num_blocks;
+  p.max_pages = max_pages;
+  p.causal = causal ? 1 : 0;
+  p.always_partial = 1;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.block_table = block_table;
+  p.kcache = static_cast<const uint8_t*>(kcache);
+  p.seqlens = cache_seqlens;
+  p.metadata = metadata;
+  p.num_splits = num_splits;
+  p.ws_o = reinterpret_cast<float*>(ws + w.o_off);
+  p.ws_lse = reinterpret_cast<float*>(ws + w.lse_off);
+  p.trace = t_trace;
+  p.trace_plane = trace_plane;
+  p.n_prefix = su.n_prefix;
+  p.own_groups = su.own_groups;
+  p.total_rows = batch * p.R;
+  p.prefix_len = prefix_len;
+  p.prefix_pages = prefix_pages;
+  p.prefix_table = prefix_table;
+  if ((rc = launch_pair_decode<false, true>(q, kcache, tkv, p, st)) != MLA_OK) return rc;
+
+  mla::SharedCombineParams c{};
+  c.units = su.units;
+  c.n_prefix = su.n_prefix;
+  c.own_groups = su.own_groups;
+  c.R = p.R;
+  c.total_rows = p.total_rows;
+  c.metadata = metadata;
+  c.num_splits = num_splits;
+  c.ws_o = p.ws_o;
+  c.ws_lse = p.ws_lse;
+  c.out = static_cast<__nv_bfloat16*>(out);
+  c.lse = lse;
+  int dev = 0, sms = 0;
+  MLA_CUDA(cudaGetDevice(&dev));
+  MLA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  if (p.total_rows < 8 * sms) {
+    PdlLaunch L(dim3(p.total_rows), dim3(mla::kCombineThreads), 0, st);
+    MLA_CUDA(cudaLaunchKernelEx(&L.cfg, mla::mla_shared_combine_kernel<true>, c));
+  } else {
+    PdlLaunch L(dim3(mla::ceil_div(p.total_rows, mla::kCombineWarps)), dim3(mla::kCombineThreads),
+                0, st);
+    MLA_CUDA(cudaLaunchKernelEx(&L.cfg, mla::mla_shared_combine_kernel<false>, c));
+  }
+  return MLA_OK;
 }
 
 int mla_cache_append(const void* kv, int64_t kv_stride, int d, const int32_t* slots,

@@ -98,6 +98,17 @@ __device__ __forceinline__ bool sm_wait_cluster(uint64_t* bar, uint32_t parity, 
   return all != 0;
 }
 
+// Shared prefix: the sequence of an own-token unit, and a unit's first query
+// row (of all batch * R).
+__device__ __forceinline__ int own_seq(const DecodeParams& P, int unit) {
+  return (unit - P.n_prefix) / P.own_groups;
+}
+__device__ __forceinline__ int shared_row0(const DecodeParams& P, int unit) {
+  if (unit < P.n_prefix) return unit * 128;
+  const int b = own_seq(P, unit);
+  return b * P.R + (unit - P.n_prefix - b * P.own_groups) * 128;
+}
+
 // Warp-uniform bounded wait (every lane waits, the warp agrees).
 __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, int site) {
   const bool mine = ptx::mbar_wait_cluster(bar, parity, site);
@@ -108,7 +119,11 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
 // index lists (sparse prefill): K and V come in by TMA gather4 loads of four
 // rows at a time (tm_kv is then a map with a box one row high), and entries
 // that name no row are masked.
-template <bool kGather>
+//
+// kShared: the batch shares a prefix.  A unit is 128 query rows, of any
+// sequences, over the prefix, or up to 128 rows of one sequence over its own
+// tokens; every unit writes partials, merged by mla_shared_combine_kernel.
+template <bool kGather, bool kShared = false>
 __global__ void __launch_bounds__(pcfg::kThreads, 1)
     mla_pair_decode_kernel(const __grid_constant__ CUtensorMap tm_q3,
                            const __grid_constant__ CUtensorMap tm_kv,
@@ -135,6 +150,14 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
   ptx::grid_dep_launch();  // the combine grid may be scheduled as CTAs retire
   const int32_t* meta = P.metadata + part * kMetaInts;
   if (meta[0] > meta[2]) return;  // empty part: both CTAs of the pair leave together
+  constexpr Mode kUnits = kShared ? kSharedPrefix : kDense;
+  if constexpr (kShared) {
+    // a plan made for other units names none of these: leave (both CTAs alike)
+    if (meta[5] != P.batch) {
+      if (threadIdx.x == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x47);
+      return;
+    }
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNStage; ++i) {
@@ -180,7 +203,14 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
     const int npg = (un.L + kPage - 1) / kPage;  // <= max_pages
     const int end = min(npg, 2 * un.hi);
     const int pg = page < end ? page : fallback;
-    const int blk = pg < npg ? P.block_table[(size_t)un.b * P.max_pages + pg] : 0;
+    const int32_t* table = P.block_table;
+    if constexpr (kShared) {
+      table = un.b < P.n_prefix ? P.prefix_table
+                                : table + (size_t)own_seq(P, un.b) * P.max_pages;
+    } else {
+      table += (size_t)un.b * P.max_pages;
+    }
+    const int blk = pg < npg ? table[pg] : 0;
     return clamp_block(blk, P.num_blocks);
   };
   // Gather mode: the row of index entry e of unit `un` (row 0, masked, for an
@@ -194,7 +224,14 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
   // are not recorded).
   auto trace_if_real = [&](const Unit& un, int page, int blk, int planes) {
     const int npg = (un.L + kPage - 1) / kPage;
-    if (page < npg && page < 2 * un.hi) trace_page(P, un.b, page, blk, planes);
+    if (page >= npg || page >= 2 * un.hi) return;
+    if constexpr (kShared) {
+      const bool prefix = un.b < P.n_prefix;
+      trace_page(P, prefix ? 0 : own_seq(P, un.b), page, blk, planes,
+                 prefix ? 0 : (size_t)P.prefix_pages * kPage);
+    } else {
+      trace_page(P, un.b, page, blk, planes);
+    }
   };
 
   if (warp == 0 || warp >= 2 + kSoftmaxWarps) {
@@ -328,14 +365,15 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
         }
       return true;
     };
-    while (ok && it.next<kDense>(P, u)) {
+    while (ok && it.next<kUnits>(P, u)) {
       const int n = (u.hi - u.lo + 1) >> 1;
       if (role == 0) {
         if (!warp_wait_cluster(&C.q_empty, (u_idx & 1) ^ 1, 0x42)) {
           ok = false;
           break;
         }
-        const int row0 = u.b * P.R + grp * 128 + static_cast<int>(rank) * kRows;
+        const int row0 = (kShared ? shared_row0(P, u.b) : u.b * P.R + grp * 128) +
+                         static_cast<int>(rank) * kRows;
         if (ptx::elect_one_sync()) {
           if (leader) ptx::mbar_arrive_expect_tx(&C.q_full, 2u * nqk * kBox);
           ptx::tma_load_3d_pair(sQ, &tm_q3, leader_addr(&C.q_full), 0, row0, 0);
@@ -439,7 +477,7 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
         }
         return true;
       };
-      while (ok && it.next<kDense>(P, u)) {
+      while (ok && it.next<kUnits>(P, u)) {
         if (!warp_wait_cluster(&C.q_full, u_idx & 1, 0x54)) break;
         ptx::tc_fence_after();
         const int n = (u.hi - u.lo + 1) >> 1;
@@ -490,8 +528,9 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
     const int h = L >> 6;           // lane half
     const int quarter = 2 * h + wg;  // the thread's quarter of a row's S columns
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const int rg = grp * 128 + static_cast<int>(rank) * kRows + r;  // row in [0, R)
-    const bool row_valid = rg < P.R;
+    const int r128 = static_cast<int>(rank) * kRows + r;  // row of the unit
+    const int rg = grp * 128 + r128;                      // row in [0, R)
+    bool row_valid = rg < P.R;
     const uint32_t s_empty_l = leader_addr(&C.s_empty[0]);
     const uint32_t p_full_l = leader_addr(&C.p_full);
     const uint32_t o_free_l = leader_addr(&C.o_free);
@@ -499,10 +538,25 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
     int u_idx = 0;
     Unit u;
     bool ok = true;
-    while (ok && it.next<kDense>(P, u)) {
+    while (ok && it.next<kUnits>(P, u)) {
       const int n = (u.hi - u.lo + 1) >> 1;
       int lim = 0;
-      if (row_valid) {
+      if constexpr (kShared) {
+        // query t of s_q sees the first prefix + own - s_q + 1 + t tokens
+        const bool prefix = u.b < P.n_prefix;
+        const int row = shared_row0(P, u.b) + r128;  // of all rows
+        const int b = prefix ? row / P.R : own_seq(P, u.b);
+        row_valid = prefix ? row < P.total_rows : row < (b + 1) * P.R;
+        if (row_valid) {
+          lim = u.L;
+          if (P.causal) {
+            int seen = u.L;  // by the last query, of this unit's tokens and those before
+            if (prefix) seen += max(0, min(P.seqlens[b], P.max_pages * kPage));
+            lim = min(lim, seen - P.s_q + 1 + (row - b * P.R) / P.h_q);
+          }
+          lim = min(max(lim, 0), u.hi * kTileT);
+        }
+      } else if (row_valid) {
         lim = P.causal ? u.L - P.s_q + 1 + rg / P.h_q : u.L;
         lim = lim < 0 ? 0 : lim;
         lim = min(lim, u.hi * kTileT);  // tokens of later splits belong to them
@@ -625,7 +679,9 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       const bool partial = P.always_partial || u.nsplit > 1;
-      const int ws_row = ((P.ws_base ? P.ws_base[u.b] : P.num_splits[u.b]) + u.split) * P.R + rg;
+      const int ws_row =
+          kShared ? (P.num_splits[u.b] + u.split) * 128 + r128
+                  : ((P.ws_base ? P.ws_base[u.b] : P.num_splits[u.b]) + u.split) * P.R + rg;
       float inv = l > 0.f ? 1.0f / l : 0.f;
       float lv = l > 0.f ? (m_used + __log2f(l)) * 0.69314718055994531f : -INFINITY;
       if (!partial && P.sink) {
