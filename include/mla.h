@@ -339,6 +339,55 @@ MLA_API int mla_shared_prefix_decode_fwd(const void* q, const void* kcache, int 
                                          size_t workspace_bytes, void* out, float* lse,
                                          void* stream);
 
+/* Page keys for mla_page_sparse_decode: per cache block one int8 key of 576
+ * codes and an fp32 scale, the quantised mean of the block's rows:
+ *   m = mean of the rows that the sequence has in the page (formed in fp64,
+ *   rounded to fp32), scale = max|m| * (1/127) in fp32 (1 where that is 0),
+ *   code = m / scale rounded to the nearest, ties to even
+ * Recomputes the last `tail_pages` pages of every sequence (all of them where
+ * it has fewer).  After appending n tokens to each sequence, tail_pages =
+ * ceil(n / 64) + 1 covers every page that changed.
+ *   kcache, num_blocks, block_table, max_pages, cache_seqlens: as in
+ *                 mla_decode_fwd, the lengths after the append
+ *   page_keys     int8[num_blocks][576], 16-byte aligned; page_scales
+ *                 fp32[num_blocks]; only the named pages' entries are written
+ * One launch on `stream`.  batch <= 65535. */
+MLA_API int mla_page_keys_update(const void* kcache, int num_blocks, const int32_t* block_table,
+                                 int max_pages, const int32_t* cache_seqlens, int batch,
+                                 int tail_pages, int8_t* page_keys, float* page_scales,
+                                 void* stream);
+
+/* Workspace bytes for mla_page_sparse_decode. */
+MLA_API int mla_page_sparse_workspace_size(int batch, int s_q, int h_q, int d_v, int max_pages,
+                                           int topk_pages, int num_sm_parts, size_t* bytes);
+
+/* Sparse decode over whole pages: each query attends to the page that ends its
+ * tokens and to the topk_pages - 1 pages before it of highest score; of equal
+ * scores the lowest page is taken.  The score of page p is
+ *   max over heads h of (s_h * (q8_h . k8_p)) * page_scales[p]
+ * with q8_h, s_h the query row's int8 codes and scale, formed as a page key's
+ * are, every product and comparison in fp32 in this order (the integer dot
+ * products are exact), so that the selection is reproducible.
+ *   page_keys, page_scales: from mla_page_keys_update; values must be finite,
+ *                 scales > 0
+ *   topk_pages    >= 1; a query that sees no more pages than that attends to
+ *                 all of its tokens, as in mla_decode_fwd
+ *   pages         int32[batch, s_q, topk_pages] or NULL: the pages taken (page
+ *                 numbers of the sequence, ascending, -1 behind them)
+ *   num_sm_parts  from mla_num_sm_parts(device, h_q, 1)
+ *   workspace     >= mla_page_sparse_workspace_size() bytes, 256-byte aligned
+ *   d_v           512 or 576; q, kcache, block_table, cache_seqlens, out, lse,
+ *                 causal: as in mla_decode_fwd
+ * batch * s_q <= 8192.  Ownership and errors as in mla_sparse_decode. */
+MLA_API int mla_page_sparse_decode(const void* q, const void* kcache, int num_blocks,
+                                   const int8_t* page_keys, const float* page_scales,
+                                   const int32_t* block_table, int max_pages,
+                                   const int32_t* cache_seqlens, int batch, int s_q, int h_q,
+                                   int h_kv, int d_v, int topk_pages, float softmax_scale,
+                                   int causal, int num_sm_parts, void* workspace,
+                                   size_t workspace_bytes, int32_t* pages, void* out, float* lse,
+                                   void* stream);
+
 /* Appends tokens to a paged latent cache: RMSNorm of the compressed latent,
  * rotation of its RoPE dims at the token's position, quantisation to the
  * cache's row format and the write to the token's slot, in one launch
@@ -431,6 +480,9 @@ MLA_API int mla_set_kernel_events(void* start_event, void* stop_event);
  *               shared-prefix decode: N = (ceil(prefix_len / 64) + batch *
  *                 max_pages) * 64: the prefix's tokens, then the sequences'
  *                 own ones laid out as in dense decode
+ *               page-selected decode: N = batch * s_q * min(topk_pages,
+ *                 max_pages) * 64, as dense decode over each query's taken
+ *                 pages (room for batch * s_q * max_pages * 64 is asked for)
  *               sparse decode and fused sparse decode: N = batch * s_q *
  *                 topk; entry p * topk + j holds the slot entry j of query p
  *                 read (-1 if unused or out of range) in plane 0, and the row

@@ -36,6 +36,7 @@ EXPORTED = [
     "mla_sparse_prefill_fwd", "mla_set_slot_trace", "mla_cache_append",
     "mla_shared_prefix_metadata_size", "mla_shared_prefix_get_metadata",
     "mla_shared_prefix_workspace_size", "mla_shared_prefix_decode_fwd",
+    "mla_page_keys_update", "mla_page_sparse_workspace_size", "mla_page_sparse_decode",
 ]
 
 
@@ -95,6 +96,10 @@ def lib():
         L.mla_shared_prefix_decode_fwd.argtypes = [
             vp, vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32, f32, i32, vp, vp, i32, vp,
             sz, vp, vp, vp]
+        L.mla_page_keys_update.argtypes = [vp, i32, vp, i32, vp, i32, i32, vp, vp, vp]
+        L.mla_page_sparse_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32, szp]
+        L.mla_page_sparse_decode.argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, i32,
+                                             i32, i32, f32, i32, i32, vp, sz, vp, vp, vp, vp]
         L.mla_device_status.argtypes = [ip, i32]
         L.mla_noalloc_scratch_bytes.argtypes = []
         L.mla_set_kernel_events.argtypes = [vp, vp]
@@ -563,6 +568,89 @@ def mla_shared_prefix_decode_fwd(q: torch.Tensor, kcache: torch.Tensor,
           int(causal), metadata.data_ptr(), num_splits.data_ptr(), num_sm_parts, ws.data_ptr(),
           ws.numel() * ws.element_size(), out.data_ptr(), lse.data_ptr())
     return out, lse
+
+
+# ------------------------------------------------------------------ page selection
+
+def _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, dev):
+    _require(kcache.is_cuda and kcache.dim() == 4 and kcache.shape[1] == 64 and
+             kcache.shape[-1] == D_QK and kcache.dtype == torch.bfloat16 and
+             kcache.is_contiguous() and kcache.device == dev,
+             f"kcache must be contiguous [NB, 64, 1, 576] bf16 on {dev}")
+    nb = kcache.shape[0]
+    _require(tuple(page_keys.shape) == (nb, D_QK) and page_keys.dtype == torch.int8 and
+             page_keys.is_contiguous() and page_keys.device == dev,
+             f"page_keys must be contiguous int8 [{nb}, 576] on {dev}")
+    _require(tuple(page_scales.shape) == (nb,) and page_scales.dtype == torch.float32 and
+             page_scales.is_contiguous() and page_scales.device == dev,
+             f"page_scales must be contiguous fp32 [{nb}] on {dev}")
+    _require(block_table.dim() == 2, "block_table must be [b, max_pages]")
+    b = block_table.shape[0]
+    return (_int32(block_table, "block_table", block_table.shape, dev),
+            _int32(cache_seqlens, "cache_seqlens", (b,), dev))
+
+
+def mla_page_keys_update(kcache: torch.Tensor, block_table: torch.Tensor,
+                         cache_seqlens: torch.Tensor, page_keys: torch.Tensor,
+                         page_scales: torch.Tensor, tail_pages: Optional[int] = None):
+    """Recompute the int8 page keys (the quantised mean of each page's rows) of
+    the last `tail_pages` pages of every sequence (default: all pages).
+    page_keys [NB, 576] int8 and page_scales [NB] fp32 are written in place."""
+    _require(kcache.dim() == 4 and kcache.shape[2] == 1, "kcache must be [NB, 64, 1, 576]")
+    dev = kcache.device
+    bt, sl = _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, dev)
+    _call(dev, lib().mla_page_keys_update, kcache.data_ptr(), kcache.shape[0], bt.data_ptr(),
+          bt.shape[1], sl.data_ptr(), bt.shape[0],
+          bt.shape[1] if tail_pages is None else tail_pages, page_keys.data_ptr(),
+          page_scales.data_ptr())
+
+
+def mla_page_sparse_workspace_size(batch, s_q, h_q, d_v, max_pages, topk_pages,
+                                   num_sm_parts) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().mla_page_sparse_workspace_size(int(batch), int(s_q), int(h_q), int(d_v),
+                                                int(max_pages), int(topk_pages),
+                                                int(num_sm_parts), ctypes.byref(out)))
+    return out.value
+
+
+def mla_page_sparse_decode(q: torch.Tensor, kcache: torch.Tensor, page_keys: torch.Tensor,
+                           page_scales: torch.Tensor, block_table: torch.Tensor,
+                           cache_seqlens: torch.Tensor, topk_pages: int, causal: bool = True,
+                           softmax_scale: Optional[float] = None, d_v: int = 512,
+                           num_sm_parts: Optional[int] = None, pages=None, out=None, lse=None,
+                           workspace=None):
+    """Decode over the `topk_pages` pages that each query's page scores select
+    (the page that ends its tokens among them).  q [b, s_q, h_q, 576] bf16;
+    page_keys, page_scales from mla_page_keys_update; the rest as in
+    mla_decode_fwd.  Returns (out [b, s_q, h_q, d_v] bf16, lse [b, s_q, h_q]
+    fp32, pages [b, s_q, topk_pages] int32: the pages taken, ascending, -1
+    behind them)."""
+    _require(q.is_cuda and q.dim() == 4 and q.shape[-1] == D_QK and q.dtype == torch.bfloat16,
+             "q must be CUDA bf16 [b, s_q, h_q, 576]")
+    b, s_q, h_q, _ = q.shape
+    dev = q.device
+    bt, sl = _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, dev)
+    _require(bt.shape[0] == b, f"block_table must be [{b}, max_pages]")
+    q = q.contiguous()
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D_QK)
+    if num_sm_parts is None:
+        num_sm_parts = mla_num_sm_parts(h_q, 1, dev)
+    if out is None:
+        out = torch.empty((b, s_q, h_q, d_v), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((b, s_q, h_q), dtype=torch.float32, device=dev)
+    if pages is None:
+        pages = torch.empty((b, s_q, topk_pages), dtype=torch.int32, device=dev)
+    ws = _workspace(mla_page_sparse_workspace_size(b, s_q, h_q, d_v, bt.shape[1], topk_pages,
+                                                   num_sm_parts), dev, workspace)
+    _call(dev, lib().mla_page_sparse_decode, q.data_ptr(), kcache.data_ptr(), kcache.shape[0],
+          page_keys.data_ptr(), page_scales.data_ptr(), bt.data_ptr(), bt.shape[1], sl.data_ptr(),
+          b, s_q, h_q, kcache.shape[2], d_v, topk_pages, softmax_scale, int(causal), num_sm_parts,
+          ws.data_ptr(), ws.numel() * ws.element_size(), pages.data_ptr(), out.data_ptr(),
+          lse.data_ptr())
+    return out, lse, pages
 
 
 # ------------------------------------------------------------------ cache writers

@@ -16,6 +16,7 @@
 #include "combine_kernel.cuh"
 #include "decode_kernel.cuh"
 #include "page_kernel.cuh"
+#include "page_select.cuh"
 #include "pair_kernel.cuh"
 #include "prologue_kernel.cuh"
 #include "prefill_kernel.cuh"
@@ -603,6 +604,28 @@ int shared_units(int batch, int rows_per_kv, int prefix_len, SharedUnits* su) {
   su->own_groups = static_cast<int>(groups);
   su->units = static_cast<int>(n_prefix + batch * groups);
   return MLA_OK;
+}
+
+// Page-selected decode workspace: the scores [pairs, max_pages], the taken
+// pages' block table and lengths, the split tables, the dense workspace.
+struct PageSparseWs {
+  size_t scores_off, table_off, len_off, meta_off, splits_off, dense_off, dense_bytes, total;
+  int width;
+};
+
+PageSparseWs page_sparse_ws_layout(int pairs, int h_q, int d_v, int max_pages, int topk,
+                                   int parts) {
+  PageSparseWs w{};
+  w.width = topk < max_pages ? topk : max_pages;
+  w.scores_off = 0;
+  w.table_off = align_up(static_cast<size_t>(pairs) * max_pages * 4, 256);
+  w.len_off = w.table_off + align_up(static_cast<size_t>(pairs) * w.width * 4, 256);
+  w.meta_off = w.len_off + align_up(static_cast<size_t>(pairs) * 4, 256);
+  w.splits_off = w.meta_off + align_up(static_cast<size_t>(parts) * mla::kMetaInts * 4, 256);
+  w.dense_off = w.splits_off + align_up((static_cast<size_t>(pairs) + 1) * 4, 256);
+  w.dense_bytes = dense_ws_layout(pairs, h_q, d_v, parts).total;
+  w.total = w.dense_off + w.dense_bytes;
+  return w;
 }
 
 }  // namespace
@@ -1254,6 +1277,136 @@ int mla_shared_prefix_decode_fwd(const void* q, const void* kcache, int num_bloc
     MLA_CUDA(cudaLaunchKernelEx(&L.cfg, mla::mla_shared_combine_kernel<false>, c));
   }
   return MLA_OK;
+}
+
+int mla_page_keys_update(const void* kcache, int num_blocks, const int32_t* block_table,
+                         int max_pages, const int32_t* cache_seqlens, int batch, int tail_pages,
+                         int8_t* page_keys, float* page_scales, void* stream) {
+  MLA_CHECK_ARG(batch >= 0 && batch <= 65535, "batch must be in [0, 65535] (got %d)", batch);
+  MLA_CHECK_ARG(max_pages >= 1 && static_cast<long long>(max_pages) * mla::kPage < (1LL << 31),
+                "max_pages must be in [1, 2^31 / 64) (got %d)", max_pages);
+  MLA_CHECK_ARG(num_blocks >= 1 && static_cast<long long>(num_blocks) * mla::kPage < (1LL << 31),
+                "num_blocks must be in [1, 2^31 / 64) (got %d)", num_blocks);
+  MLA_CHECK_ARG(tail_pages >= 1, "tail_pages must be >= 1 (got %d)", tail_pages);
+  MLA_CHECK_ARG(kcache && block_table && cache_seqlens && page_keys && page_scales,
+                "null device pointer");
+  MLA_CHECK_ARG(aligned(kcache, 16) && aligned(page_keys, 16),
+                "kcache and page_keys must be 16-byte aligned");
+  MLA_CHECK_ARG(aligned(block_table, 4) && aligned(cache_seqlens, 4) && aligned(page_scales, 4),
+                "block_table, cache_seqlens and page_scales must be 4-byte aligned");
+  if (batch == 0) return MLA_OK;
+  mla::PageKeysParams p{};
+  p.kcache = static_cast<const __nv_bfloat16*>(kcache);
+  p.num_blocks = num_blocks;
+  p.block_table = block_table;
+  p.max_pages = max_pages;
+  p.seqlens = cache_seqlens;
+  p.tail = tail_pages < max_pages ? tail_pages : max_pages;
+  p.keys = page_keys;
+  p.scales = page_scales;
+  // an ordinary launch: earlier work of the stream may be writing the cache
+  mla::mla_page_keys_kernel<<<dim3(p.tail, batch), mla::kKeyThreads, 0,
+                              static_cast<cudaStream_t>(stream)>>>(p);
+  MLA_CUDA(cudaGetLastError());
+  return MLA_OK;
+}
+
+int mla_page_sparse_workspace_size(int batch, int s_q, int h_q, int d_v, int max_pages,
+                                   int topk_pages, int num_sm_parts, size_t* bytes) {
+  MLA_CHECK_ARG(bytes, "bytes is null");
+  MLA_CHECK_ARG(batch >= 0 && s_q >= 1 && h_q >= 1 && max_pages >= 1 && topk_pages >= 1 &&
+                    num_sm_parts >= 1 &&
+                    static_cast<long long>(batch) * s_q <= mla::kPlanMaxBatch,
+                "bad sizes");
+  MLA_CHECK_ARG(d_v == 512 || d_v == 576, "d_v must be 512 or 576 (got %d)", d_v);
+  *bytes = page_sparse_ws_layout(batch * s_q, h_q, d_v, max_pages, topk_pages, num_sm_parts).total;
+  return MLA_OK;
+}
+
+int mla_page_sparse_decode(const void* q, const void* kcache, int num_blocks,
+                           const int8_t* page_keys, const float* page_scales,
+                           const int32_t* block_table, int max_pages,
+                           const int32_t* cache_seqlens, int batch, int s_q, int h_q, int h_kv,
+                           int d_v, int topk_pages, float softmax_scale, int causal,
+                           int num_sm_parts, void* workspace, size_t workspace_bytes,
+                           int32_t* pages, void* out, float* lse, void* stream) {
+  if (h_kv != 1) return fail(MLA_ERR_UNSUPPORTED, "h_kv must be 1 (got %d)", h_kv);
+  MLA_CHECK_ARG(batch >= 0 && s_q >= 1 && h_q >= 1, "bad sizes");
+  MLA_CHECK_ARG(static_cast<long long>(batch) * s_q <= mla::kPlanMaxBatch,
+                "at most %d (sequence, query) pairs (got %lld)", mla::kPlanMaxBatch,
+                static_cast<long long>(batch) * s_q);
+  MLA_CHECK_ARG(topk_pages >= 1, "topk_pages must be >= 1 (got %d)", topk_pages);
+  MLA_CHECK_ARG(page_keys && page_scales, "null device pointer argument");
+  MLA_CHECK_ARG(aligned(page_keys, 16), "page_keys must be 16-byte aligned");
+  MLA_CHECK_ARG(aligned(page_scales, 4) && aligned(pages, 4),
+                "page_scales and pages must be 4-byte aligned");
+  MLA_CHECK_ARG(workspace && aligned(workspace, 256), "workspace must be 256-byte aligned");
+  MLA_CHECK_ARG(max_pages >= 1, "max_pages must be >= 1 (got %d)", max_pages);
+  MLA_CHECK_ARG(num_sm_parts >= 1 && num_sm_parts <= mla::kCombineMaxSplits,
+                "num_sm_parts must be in [1, %d] (got %d)", mla::kCombineMaxSplits, num_sm_parts);
+  MLA_CHECK_ARG(d_v == 512 || d_v == 576, "d_v must be 512 or 576 (got %d)", d_v);
+  MLA_CHECK_ARG(block_table && cache_seqlens && aligned(block_table, 4) &&
+                    aligned(cache_seqlens, 4),
+                "block_table or cache_seqlens is null or misaligned");
+  const int pairs = batch * s_q;
+  const PageSparseWs w =
+      page_sparse_ws_layout(pairs, h_q, d_v, max_pages, topk_pages, num_sm_parts);
+  MLA_CHECK_ARG(workspace_bytes >= w.total, "workspace too small: %zu < %zu", workspace_bytes,
+                w.total);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int32_t* table = reinterpret_cast<int32_t*>(ws + w.table_off);
+  int32_t* lens = reinterpret_cast<int32_t*>(ws + w.len_off);
+  int32_t* meta = reinterpret_cast<int32_t*>(ws + w.meta_off);
+  int32_t* splits = reinterpret_cast<int32_t*>(ws + w.splits_off);
+  // every check of the decode over the taken pages, before anything is launched
+  int rc = check_dense_decode(q, kcache, table, max_pages, num_blocks, lens, pairs, 1, h_q, h_kv,
+                              d_v, softmax_scale, meta, splits, num_sm_parts, ws + w.dense_off,
+                              w.dense_bytes, out, lse);
+  if (rc != MLA_OK) return rc;
+  if (pairs == 0) return MLA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  mla::PageSelectParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.keys = page_keys;
+  p.scales = page_scales;
+  p.num_blocks = num_blocks;
+  p.block_table = block_table;
+  p.max_pages = max_pages;
+  p.seqlens = cache_seqlens;
+  p.s_q = s_q;
+  p.h_q = h_q;
+  p.causal = causal ? 1 : 0;
+  p.topk = topk_pages;
+  p.width = w.width;
+  p.scores = reinterpret_cast<float*>(ws + w.scores_off);
+  p.taken_table = table;
+  p.taken_lens = lens;
+  p.pages = pages;
+  if (topk_pages < max_pages) {  // otherwise every page is taken
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+      attr_err = cudaFuncSetAttribute(mla::mla_page_score_kernel,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      mla::kScoreSmem);
+    });
+    if (attr_err != cudaSuccess)
+      return fail(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+    // an ordinary launch: earlier work of the stream may be writing the inputs
+    mla::mla_page_score_kernel<<<dim3(mla::ceil_div(max_pages, mla::kScorePages), pairs),
+                                 mla::kScoreThreads, mla::kScoreSmem, st>>>(p);
+    MLA_CUDA(cudaGetLastError());
+    PdlLaunch L(dim3(pairs), dim3(mla::kSelectThreads), 0, st);
+    MLA_CUDA(cudaLaunchKernelEx(&L.cfg, mla::mla_page_select_kernel, p));
+  } else {
+    mla::mla_page_select_kernel<<<pairs, mla::kSelectThreads, 0, st>>>(p);
+    MLA_CUDA(cudaGetLastError());
+  }
+  if ((rc = mla_get_metadata(lens, pairs, h_q, 1, num_sm_parts, meta, splits, stream)) != MLA_OK)
+    return rc;
+  return mla_decode_fwd(q, kcache, table, w.width, num_blocks, lens, pairs, 1, h_q, 1, d_v,
+                        softmax_scale, 0, meta, splits, num_sm_parts, ws + w.dense_off,
+                        w.dense_bytes, out, lse, stream);
 }
 
 int mla_cache_append(const void* kv, int64_t kv_stride, int d, const int32_t* slots,
