@@ -127,13 +127,15 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _call(device, fn, *args):
-    """fn(*args, stream) with `device` current, on its current stream."""
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+def _call(index, fn, *args):
+    """fn(*args, stream) with device `index` current, on its current stream."""
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        _check(fn(*args, torch.cuda.current_stream().cuda_stream))
+        with torch.cuda.device(index):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != MLA_OK:
+        _check(rc)
 
 
 def _require(cond, msg):
@@ -490,6 +492,39 @@ def mla_sparse_prefill_fwd(q, kv, indices, softmax_scale=None, d_v=512, topk_len
     return out, lse
 
 
+SOFTMAX_SCALE = 1.0 / math.sqrt(D_QK)
+
+
+def _int32(t, name, shape, index):
+    """`t` as a contiguous int32 tensor of `shape` on device `index`."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+    if t.dtype != torch.int32:
+        if t.dtype != torch.int64:
+            raise ValueError(f"{name} must be int32 (or int64)")
+        t = t.to(torch.int32)
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _query(q):
+    """(device index, shape) of a CUDA bf16 [b, s_q, h_q, 576] query."""
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != D_QK or q.dtype != torch.bfloat16 or not q.is_cuda:
+        raise ValueError("q must be CUDA bf16 [b, s_q, h_q, 576]")
+    return q.get_device(), shape
+
+
+def _bf16_cache(kcache, index):
+    shape = kcache.shape
+    if len(shape) != 4 or shape[1] != 64 or shape[3] != D_QK or \
+            kcache.dtype != torch.bfloat16 or not kcache.is_contiguous() or index < 0 or \
+            kcache.get_device() != index:
+        raise ValueError("kcache must be contiguous CUDA bf16 [NB, 64, h_kv, 576] on the "
+                         "queries' device")
+
+
 # ------------------------------------------------------------------ shared prefix
 
 def mla_shared_prefix_workspace_size(batch, rows_per_kv, prefix_len, num_sm_parts) -> int:
@@ -516,7 +551,7 @@ def mla_shared_prefix_get_metadata(cache_seqlens: torch.Tensor, prefix_len: int,
                                                  ctypes.byref(n)))
     meta = torch.empty((num_sm_parts, 8), dtype=torch.int32, device=sl.device)
     splits = torch.empty((n.value // 4,), dtype=torch.int32, device=sl.device)
-    _call(sl.device, lib().mla_shared_prefix_get_metadata, sl.data_ptr(), sl.numel(),
+    _call(sl.get_device(), lib().mla_shared_prefix_get_metadata, sl.data_ptr(), sl.numel(),
           int(rows_per_kv), int(h_kv), int(prefix_len), int(num_sm_parts), meta.data_ptr(),
           splits.data_ptr())
     return meta, splits, num_sm_parts
@@ -534,60 +569,55 @@ def mla_shared_prefix_decode_fwd(q: torch.Tensor, kcache: torch.Tensor,
     blocks of the prefix; block_table [b, max_pages] and cache_seqlens [b] int32
     the sequences' own tokens behind it.  Returns (out [b, s_q, h_q, 512] bf16,
     lse [b, s_q, h_q] fp32)."""
-    _require(q.is_cuda and q.dim() == 4 and q.shape[-1] == D_QK and q.dtype == torch.bfloat16,
-             "q must be CUDA bf16 [b, s_q, h_q, 576]")
-    _require(kcache.dim() == 4 and kcache.shape[1] == 64 and kcache.shape[-1] == D_QK and
-             kcache.dtype == torch.bfloat16 and kcache.is_contiguous(),
-             "kcache must be contiguous [NB, 64, h_kv, 576] bf16")
-    b, s_q, h_q, _ = q.shape
-    dev = q.device
-    _require(block_table.dim() == 2, "block_table must be [b, max_pages]")
-    bt = _int32(block_table, "block_table", (b, block_table.shape[1]), dev)
-    sl = _int32(cache_seqlens, "cache_seqlens", (b,), dev)
+    index, (b, s_q, h_q, _) = _query(q)
+    _bf16_cache(kcache, index)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [b, max_pages]")
+    bt = _int32(block_table, "block_table", (b, block_table.shape[1]), index)
+    sl = _int32(cache_seqlens, "cache_seqlens", (b,), index)
     pt = None
     if prefix_len > 0:
-        _require(prefix_table is not None and prefix_table.dim() == 1 and
-                 prefix_table.numel() >= -(-prefix_len // 64),
-                 "prefix_table must be [>= ceil(prefix_len / 64)]")
-        pt = _int32(prefix_table, "prefix_table", prefix_table.shape, dev)
-    _require(metadata.numel() >= 8 * num_sm_parts and metadata.dtype == torch.int32 and
-             num_splits.dtype == torch.int32 and metadata.device == dev and
-             num_splits.device == dev, f"metadata and num_splits must be the plan, on {dev}")
-    q = q.contiguous()
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(D_QK)
+        if prefix_table is None or prefix_table.dim() != 1 or \
+                prefix_table.numel() < -(-prefix_len // 64):
+            raise ValueError("prefix_table must be [>= ceil(prefix_len / 64)]")
+        pt = _int32(prefix_table, "prefix_table", prefix_table.shape, index)
+    if metadata.numel() < 8 * num_sm_parts or metadata.dtype != torch.int32 or \
+            num_splits.dtype != torch.int32 or metadata.get_device() != index or \
+            num_splits.get_device() != index:
+        raise ValueError(f"metadata and num_splits must be the plan, on cuda:{index}")
+    if not q.is_contiguous():
+        q = q.contiguous()
     if out is None:
-        out = torch.empty((b, s_q, h_q, 512), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((b, s_q, h_q, 512))
     if lse is None:
-        lse = torch.empty((b, s_q, h_q), dtype=torch.float32, device=dev)
-    ws = _workspace(mla_shared_prefix_workspace_size(b, s_q * h_q, prefix_len, num_sm_parts), dev,
-                    workspace)
-    _call(dev, lib().mla_shared_prefix_decode_fwd, q.data_ptr(), kcache.data_ptr(),
+        lse = torch.empty((b, s_q, h_q), dtype=torch.float32, device=q.device)
+    ws = _workspace(mla_shared_prefix_workspace_size(b, s_q * h_q, prefix_len, num_sm_parts),
+                    q.device, workspace)
+    _call(index, lib().mla_shared_prefix_decode_fwd, q.data_ptr(), kcache.data_ptr(),
           kcache.shape[0], None if pt is None else pt.data_ptr(), prefix_len, bt.data_ptr(),
-          bt.shape[1], sl.data_ptr(), b, s_q, h_q, kcache.shape[2], 512, softmax_scale,
-          int(causal), metadata.data_ptr(), num_splits.data_ptr(), num_sm_parts, ws.data_ptr(),
+          bt.shape[1], sl.data_ptr(), b, s_q, h_q, kcache.shape[2], 512,
+          SOFTMAX_SCALE if softmax_scale is None else softmax_scale, int(causal),
+          metadata.data_ptr(), num_splits.data_ptr(), num_sm_parts, ws.data_ptr(),
           ws.numel() * ws.element_size(), out.data_ptr(), lse.data_ptr())
     return out, lse
 
 
 # ------------------------------------------------------------------ page selection
 
-def _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, dev):
-    _require(kcache.is_cuda and kcache.dim() == 4 and kcache.shape[1] == 64 and
-             kcache.shape[-1] == D_QK and kcache.dtype == torch.bfloat16 and
-             kcache.is_contiguous() and kcache.device == dev,
-             f"kcache must be contiguous [NB, 64, 1, 576] bf16 on {dev}")
+def _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, index):
+    """(blocks, block_table, cache_seqlens) once the arguments are checked."""
+    _bf16_cache(kcache, index)
     nb = kcache.shape[0]
-    _require(tuple(page_keys.shape) == (nb, D_QK) and page_keys.dtype == torch.int8 and
-             page_keys.is_contiguous() and page_keys.device == dev,
-             f"page_keys must be contiguous int8 [{nb}, 576] on {dev}")
-    _require(tuple(page_scales.shape) == (nb,) and page_scales.dtype == torch.float32 and
-             page_scales.is_contiguous() and page_scales.device == dev,
-             f"page_scales must be contiguous fp32 [{nb}] on {dev}")
-    _require(block_table.dim() == 2, "block_table must be [b, max_pages]")
-    b = block_table.shape[0]
-    return (_int32(block_table, "block_table", block_table.shape, dev),
-            _int32(cache_seqlens, "cache_seqlens", (b,), dev))
+    if page_keys.shape != (nb, D_QK) or page_keys.dtype != torch.int8 or \
+            not page_keys.is_contiguous() or page_keys.get_device() != index:
+        raise ValueError(f"page_keys must be contiguous int8 [{nb}, 576] on cuda:{index}")
+    if page_scales.shape != (nb,) or page_scales.dtype != torch.float32 or \
+            not page_scales.is_contiguous() or page_scales.get_device() != index:
+        raise ValueError(f"page_scales must be contiguous fp32 [{nb}] on cuda:{index}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [b, max_pages]")
+    bt = _int32(block_table, "block_table", block_table.shape, index)
+    return nb, bt, _int32(cache_seqlens, "cache_seqlens", (bt.shape[0],), index)
 
 
 def mla_page_keys_update(kcache: torch.Tensor, block_table: torch.Tensor,
@@ -596,13 +626,14 @@ def mla_page_keys_update(kcache: torch.Tensor, block_table: torch.Tensor,
     """Recompute the int8 page keys (the quantised mean of each page's rows) of
     the last `tail_pages` pages of every sequence (default: all pages).
     page_keys [NB, 576] int8 and page_scales [NB] fp32 are written in place."""
-    _require(kcache.dim() == 4 and kcache.shape[2] == 1, "kcache must be [NB, 64, 1, 576]")
-    dev = kcache.device
-    bt, sl = _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, dev)
-    _call(dev, lib().mla_page_keys_update, kcache.data_ptr(), kcache.shape[0], bt.data_ptr(),
-          bt.shape[1], sl.data_ptr(), bt.shape[0],
-          bt.shape[1] if tail_pages is None else tail_pages, page_keys.data_ptr(),
-          page_scales.data_ptr())
+    index = kcache.get_device()
+    nb, bt, sl = _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, index)
+    if kcache.shape[2] != 1:
+        raise ValueError("kcache must be [NB, 64, 1, 576]")
+    b, max_pages = bt.shape
+    _call(index, lib().mla_page_keys_update, kcache.data_ptr(), nb, bt.data_ptr(), max_pages,
+          sl.data_ptr(), b, max_pages if tail_pages is None else tail_pages,
+          page_keys.data_ptr(), page_scales.data_ptr())
 
 
 def mla_page_sparse_workspace_size(batch, s_q, h_q, d_v, max_pages, topk_pages,
@@ -626,44 +657,33 @@ def mla_page_sparse_decode(q: torch.Tensor, kcache: torch.Tensor, page_keys: tor
     mla_decode_fwd.  Returns (out [b, s_q, h_q, d_v] bf16, lse [b, s_q, h_q]
     fp32, pages [b, s_q, topk_pages] int32: the pages taken, ascending, -1
     behind them)."""
-    _require(q.is_cuda and q.dim() == 4 and q.shape[-1] == D_QK and q.dtype == torch.bfloat16,
-             "q must be CUDA bf16 [b, s_q, h_q, 576]")
-    b, s_q, h_q, _ = q.shape
-    dev = q.device
-    bt, sl = _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, dev)
-    _require(bt.shape[0] == b, f"block_table must be [{b}, max_pages]")
-    q = q.contiguous()
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(D_QK)
+    index, (b, s_q, h_q, _) = _query(q)
+    nb, bt, sl = _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, index)
+    if bt.shape[0] != b:
+        raise ValueError(f"block_table must be [{b}, max_pages]")
+    if not q.is_contiguous():
+        q = q.contiguous()
+    dev, max_pages = q.device, bt.shape[1]
     if num_sm_parts is None:
         num_sm_parts = mla_num_sm_parts(h_q, 1, dev)
+    nbytes = mla_page_sparse_workspace_size(b, s_q, h_q, d_v, max_pages, topk_pages, num_sm_parts)
     if out is None:
-        out = torch.empty((b, s_q, h_q, d_v), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((b, s_q, h_q, d_v))
     if lse is None:
         lse = torch.empty((b, s_q, h_q), dtype=torch.float32, device=dev)
     if pages is None:
-        pages = torch.empty((b, s_q, topk_pages), dtype=torch.int32, device=dev)
-    ws = _workspace(mla_page_sparse_workspace_size(b, s_q, h_q, d_v, bt.shape[1], topk_pages,
-                                                   num_sm_parts), dev, workspace)
-    _call(dev, lib().mla_page_sparse_decode, q.data_ptr(), kcache.data_ptr(), kcache.shape[0],
-          page_keys.data_ptr(), page_scales.data_ptr(), bt.data_ptr(), bt.shape[1], sl.data_ptr(),
-          b, s_q, h_q, kcache.shape[2], d_v, topk_pages, softmax_scale, int(causal), num_sm_parts,
+        pages = bt.new_empty((b, s_q, topk_pages))
+    ws = _workspace(nbytes, dev, workspace)
+    _call(index, lib().mla_page_sparse_decode, q.data_ptr(), kcache.data_ptr(), nb,
+          page_keys.data_ptr(), page_scales.data_ptr(), bt.data_ptr(), max_pages, sl.data_ptr(),
+          b, s_q, h_q, kcache.shape[2], d_v, topk_pages,
+          SOFTMAX_SCALE if softmax_scale is None else softmax_scale, int(causal), num_sm_parts,
           ws.data_ptr(), ws.numel() * ws.element_size(), pages.data_ptr(), out.data_ptr(),
           lse.data_ptr())
     return out, lse, pages
 
 
 # ------------------------------------------------------------------ cache writers
-
-def _int32(t, name, shape, device):
-    """`t` as a contiguous int32 tensor of `shape` on `device`."""
-    _require(tuple(t.shape) == tuple(shape), f"{name} must be {list(shape)}")
-    _require(t.device == device, f"{name} must be on {device}")
-    if t.dtype != torch.int32:
-        _require(t.dtype == torch.int64, f"{name} must be int32 (or int64)")
-        t = t.to(torch.int32)
-    return t.contiguous()
-
 
 def mla_cache_append(kv: torch.Tensor, slots: torch.Tensor, kcache: torch.Tensor,
                      positions: Optional[torch.Tensor] = None,
@@ -676,37 +696,40 @@ def mla_cache_append(kv: torch.Tensor, slots: torch.Tensor, kcache: torch.Tensor
     strided.  slots [n] int32 physical slots (negative = padding, skipped; the
     others must differ).  `rows` (bf16, kv's shape, contiguous) receives the
     rows as the cache stands for them.  Writes into `kcache`; returns `rows`."""
-    if kcache.dtype == torch.bfloat16:
-        _require(kcache.shape[-1] == D_QK, "a bf16 kcache must be [..., 576]")
+    width = kcache.shape[-1]
+    if kcache.dtype == torch.bfloat16 and width == D_QK:
         row_bytes = 2 * D_QK
+    elif kcache.dtype == torch.uint8 and width in (656, 528, 288):
+        row_bytes = width
     else:
-        _require(kcache.dtype == torch.uint8 and kcache.shape[-1] in (656, 528, 288),
-                 "kcache must be bf16 [..., 576] or uint8 [..., 656], [..., 528] or [..., 288]")
-        row_bytes = int(kcache.shape[-1])
+        raise ValueError("kcache must be bf16 [..., 576] or uint8 [..., 656], [..., 528] or "
+                         "[..., 288]")
     d = D_QK if row_bytes >= 656 else 512
-    _require(kv.is_cuda and kv.dim() == 2 and kv.shape[1] == d and kv.dtype == torch.bfloat16,
-             f"kv must be CUDA bf16 [n, {d}] for {row_bytes}-byte cache rows")
-    dev, n = kv.device, kv.shape[0]
-    _require(kcache.is_contiguous() and kcache.device == dev,
-             f"kcache must be contiguous and on {dev}")
+    shape = kv.shape
+    if len(shape) != 2 or shape[1] != d or kv.dtype != torch.bfloat16 or not kv.is_cuda:
+        raise ValueError(f"kv must be CUDA bf16 [n, {d}] for {row_bytes}-byte cache rows")
+    index, n = kv.get_device(), shape[0]
+    if not kcache.is_contiguous() or kcache.get_device() != index:
+        raise ValueError(f"kcache must be contiguous and on cuda:{index}")
     if n == 0:
         return rows
-    if kv.stride(1) != 1 or kv.stride(0) % 8 or (n > 1 and kv.stride(0) < d) or kv.data_ptr() % 16:
-        kv = kv.clone(memory_format=torch.contiguous_format)
-    slots = _int32(slots, "slots", (n,), dev)
+    stride, inner = kv.stride()
+    if inner != 1 or stride % 8 or (n > 1 and stride < d) or kv.data_ptr() % 16:
+        kv, stride = kv.clone(memory_format=torch.contiguous_format), d
+    slots = _int32(slots, "slots", (n,), index)
     if positions is not None:
-        positions = _int32(positions, "positions", (n,), dev)
+        positions = _int32(positions, "positions", (n,), index)
     if norm_gain is not None:
-        _require(tuple(norm_gain.shape) == (512,) and norm_gain.device == dev,
-                 f"norm_gain must be [512] on {dev}")
-        norm_gain = norm_gain.to(torch.float32).contiguous()
-    if rows is not None:
-        _require(tuple(rows.shape) == (n, d) and rows.dtype == torch.bfloat16 and
-                 rows.is_contiguous() and rows.device == dev,
-                 f"rows must be contiguous bf16 [{n}, {d}] on {dev}")
-    _call(dev, lib().mla_cache_append, kv.data_ptr(), max(kv.stride(0), d), d, slots.data_ptr(),
+        if norm_gain.shape != (512,) or norm_gain.get_device() != index:
+            raise ValueError(f"norm_gain must be [512] on cuda:{index}")
+        if norm_gain.dtype != torch.float32 or not norm_gain.is_contiguous():
+            norm_gain = norm_gain.to(torch.float32).contiguous()
+    if rows is not None and (rows.shape != shape or rows.dtype != torch.bfloat16 or
+                             not rows.is_contiguous() or rows.get_device() != index):
+        raise ValueError(f"rows must be contiguous bf16 [{n}, {d}] on cuda:{index}")
+    _call(index, lib().mla_cache_append, kv.data_ptr(), max(stride, d), d, slots.data_ptr(),
           None if positions is None else positions.data_ptr(),
           None if norm_gain is None else norm_gain.data_ptr(), eps, rope_base, n,
-          kcache.data_ptr(), kcache.numel() // kcache.shape[-1], row_bytes,
+          kcache.data_ptr(), kcache.numel() // width, row_bytes,
           None if rows is None else rows.data_ptr())
     return rows

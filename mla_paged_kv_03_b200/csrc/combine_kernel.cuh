@@ -247,10 +247,11 @@ __global__ void __launch_bounds__(kCombineThreads) mla_combine_kernel(const Comb
 constexpr int kPlanThreads = 256;
 constexpr int kPlanMaxBatch = 8192;  // prefix sums live in shared memory
 
-// Block-wide exclusive prefix sum of one value per thread; returns the
-// thread's exclusive sum, and the block total through *total.
+// Block-wide exclusive prefix sum of one value per thread (of kThreads);
+// returns the thread's exclusive sum, and the block total through *total.
+template <int kThreads = kPlanThreads>
 __device__ __forceinline__ int block_exclusive_scan(int v, int* total) {
-  __shared__ int s_warp[kPlanThreads / 32];
+  __shared__ int s_warp[kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -262,7 +263,7 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* total) {
   __syncthreads();
   int before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     const int t = s_warp[w];
     before += w < warp ? t : 0;
     all += t;
@@ -274,37 +275,37 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* total) {
 
 // Split-KV planner of one CTA: the closed forms of mla_common.h evaluated in
 // parallel (prefix sums by block scans, one metadata row per thread).
-// seqlens(b): the length of sequence (or unit) b.
-template <class Lengths>
+// seqlens(b): the length of sequence (or unit) b; C: batch + 1 ints of shared
+// memory.
+template <int kThreads = kPlanThreads, class Lengths>
 __device__ void plan_block(const Lengths seqlens, int batch, int num_parts, const PlanParams pp,
-                           int32_t* metadata, int32_t* num_splits, int32_t* ws_base,
+                           int32_t* C, int32_t* metadata, int32_t* num_splits, int32_t* ws_base,
                            int32_t* split_list, int list_cap) {
   const int o = pp.o, g = pp.g;
   const int u = g * kPlanTileCost;
-  __shared__ int32_t C[kPlanMaxBatch + 1];
   const int tid = threadIdx.x;
   int carry = 0;
-  for (int base = 0; base < batch; base += kPlanThreads) {
+  for (int base = 0; base < batch; base += kThreads) {
     const int b = base + tid;
     const int L = b < batch ? seqlens(b) : 0;
     const int v = b < batch ? o + u * granules_of(L, g) : 0;
     int chunk_total;
-    const int ex = block_exclusive_scan(v, &chunk_total);
+    const int ex = block_exclusive_scan<kThreads>(v, &chunk_total);
     if (b < batch) C[b] = carry + ex;
     carry += chunk_total;
   }
   if (tid == 0) C[batch] = carry;
   __syncthreads();
   const int w = plan_width(carry, num_parts, pp);
-  for (int p = tid; p < num_parts; p += kPlanThreads)
+  for (int p = tid; p < num_parts; p += kThreads)
     plan_part_row(C, batch, w, o, g, p, metadata + p * kMetaInts);
   int nsum = 0;
   if (tid == 0) num_splits[0] = 0;
-  for (int base = 0; base < batch; base += kPlanThreads) {
+  for (int base = 0; base < batch; base += kThreads) {
     const int b = base + tid;
     const int v = b < batch ? plan_last_part(C, b, w, u) - plan_first_part(C, b, w, o) + 1 : 0;
     int chunk_total;
-    const int ex = block_exclusive_scan(v, &chunk_total);
+    const int ex = block_exclusive_scan<kThreads>(v, &chunk_total);
     if (b < batch) num_splits[b + 1] = nsum + ex + v;
     nsum += chunk_total;
   }
@@ -312,11 +313,11 @@ __device__ void plan_block(const Lengths seqlens, int batch, int num_parts, cons
     // compact partial rows: only sequences split over several parts own rows
     // (at most 2 num_parts in all: a part holds at most two split segments)
     int wsum = 0;
-    for (int base = 0; base < batch; base += kPlanThreads) {
+    for (int base = 0; base < batch; base += kThreads) {
       const int b = base + tid;
       const int v = b < batch ? plan_last_part(C, b, w, u) - plan_first_part(C, b, w, o) + 1 : 0;
       int chunk_total;
-      const int ex = block_exclusive_scan(v > 1 ? v : 0, &chunk_total);
+      const int ex = block_exclusive_scan<kThreads>(v > 1 ? v : 0, &chunk_total);
       if (b < batch) ws_base[b] = wsum + ex;
       wsum += chunk_total;
     }
@@ -324,14 +325,14 @@ __device__ void plan_block(const Lengths seqlens, int batch, int num_parts, cons
   if (split_list) {
     // the split sequences in order (at most num_parts - 1: each lies across
     // a part boundary), then -1 up to list_cap
-    for (int i = tid; i < list_cap; i += kPlanThreads) split_list[i] = -1;
+    for (int i = tid; i < list_cap; i += kThreads) split_list[i] = -1;
     __syncthreads();
     int ksum = 0;
-    for (int base = 0; base < batch; base += kPlanThreads) {
+    for (int base = 0; base < batch; base += kThreads) {
       const int b = base + tid;
       const int v = b < batch ? plan_last_part(C, b, w, u) - plan_first_part(C, b, w, o) + 1 : 0;
       int chunk_total;
-      const int ex = block_exclusive_scan(v > 1 ? 1 : 0, &chunk_total);
+      const int ex = block_exclusive_scan<kThreads>(v > 1 ? 1 : 0, &chunk_total);
       if (b < batch && v > 1 && ksum + ex < list_cap) split_list[ksum + ex] = b;
       ksum += chunk_total;
     }
@@ -346,7 +347,8 @@ __global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const int32_t* s
                                                                int32_t* split_list, int list_cap) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();  // the decode grid waits for this one at its start
-  plan_block([=](int b) { return seqlens[b]; }, batch, num_parts, pp, metadata, num_splits,
+  __shared__ int32_t C[kPlanMaxBatch + 1];
+  plan_block([=](int b) { return seqlens[b]; }, batch, num_parts, pp, C, metadata, num_splits,
              ws_base, split_list, list_cap);
 }
 
@@ -359,9 +361,10 @@ __global__ void __launch_bounds__(kPlanThreads)
                            int32_t* num_splits) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
+  __shared__ int32_t C[kPlanMaxBatch + 1];
   plan_block(
       [=](int u) { return u < n_prefix ? prefix_len : seqlens[(u - n_prefix) / own_groups]; },
-      units, num_parts, pp, metadata, num_splits, nullptr, nullptr, 0);
+      units, num_parts, pp, C, metadata, num_splits, nullptr, nullptr, 0);
   __syncthreads();
   for (int p = threadIdx.x; p < num_parts; p += kPlanThreads) metadata[p * kMetaInts + 5] = units;
 }

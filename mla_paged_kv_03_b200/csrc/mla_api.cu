@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -177,6 +178,21 @@ SparseWs sparse_ws_layout(int pairs, int topk, int R, int d_v, int parts, bool v
   return w;
 }
 
+// Raises a kernel's limit of dynamic shared memory, once per device (the limit
+// belongs to the device's copy of the kernel).
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // Launch configuration with programmatic dependent launch: the kernel may
 // be scheduled before the preceding grid of the stream has finished and
 // waits for it in its first instruction (griddepcontrol.wait).
@@ -285,15 +301,7 @@ int record_stop(cudaStream_t st) { return record_event(t_kernel_stop, st); }
 template <int kMode>
 int launch_decode(const CUtensorMap& tq, const CUtensorMap& tkv, const mla::DecodeParams& p,
                   cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(mla::mla_decode_kernel<kMode>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    mla::cfg::kSmemBytes);
-  });
-  if (attr_err != cudaSuccess)
-    return fail(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  MLA_CUDA((allow_smem<mla::mla_decode_kernel<kMode>>(mla::cfg::kSmemBytes)));
   int rc = MLA_OK;
   const unsigned grid = static_cast<unsigned>(p.num_parts * p.n_groups);
   if ((rc = record_start(st)) != MLA_OK) return rc;
@@ -310,14 +318,7 @@ int launch_page_decode(const void* q, const CUtensorMap& tkv, const mla::DecodeP
   int rc = make_latent_map3(&tq3, q, static_cast<long long>(p.batch) * p.R, mla::kNumChunks,
                             Cfg::kRows);
   if (rc != MLA_OK) return rc;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(mla::mla_page_decode_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
-  });
-  if (attr_err != cudaSuccess)
-    return fail(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  MLA_CUDA((allow_smem<mla::mla_page_decode_kernel>(Cfg::kSmemBytes)));
   PdlLaunch L(dim3(static_cast<unsigned>(p.num_parts * p.n_groups)), dim3(Cfg::kThreads),
               Cfg::kSmemBytes, st);
   if ((rc = record_start(st)) != MLA_OK) return rc;
@@ -342,15 +343,7 @@ int launch_pair_decode(const void* q, const void* kcache, const CUtensorMap& tkv
   else if ((rc = make_latent_map3(&tv3, kcache, static_cast<long long>(p.num_blocks) * mla::kPage,
                                   2)) != MLA_OK)
     return rc;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(mla::mla_pair_decode_kernel<kGather, kShared>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    mla::pcfg::kSmemBytes);
-  });
-  if (attr_err != cudaSuccess)
-    return fail(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  MLA_CUDA((allow_smem<mla::mla_pair_decode_kernel<kGather, kShared>>(mla::pcfg::kSmemBytes)));
   PdlLaunch L(dim3(static_cast<unsigned>(2 * p.num_parts * p.n_groups)), dim3(mla::pcfg::kThreads),
               mla::pcfg::kSmemBytes, st, 2);
   if ((rc = record_start(st)) != MLA_OK) return rc;
@@ -1373,37 +1366,44 @@ int mla_page_sparse_decode(const void* q, const void* kcache, int num_blocks,
   p.block_table = block_table;
   p.max_pages = max_pages;
   p.seqlens = cache_seqlens;
+  p.pairs = pairs;
   p.s_q = s_q;
   p.h_q = h_q;
   p.causal = causal ? 1 : 0;
   p.topk = topk_pages;
   p.width = w.width;
-  p.scores = reinterpret_cast<float*>(ws + w.scores_off);
+  p.scores = reinterpret_cast<uint32_t*>(ws + w.scores_off);
   p.taken_table = table;
   p.taken_lens = lens;
   p.pages = pages;
-  if (topk_pages < max_pages) {  // otherwise every page is taken
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-      attr_err = cudaFuncSetAttribute(mla::mla_page_score_kernel,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      mla::kScoreSmem);
-    });
-    if (attr_err != cudaSuccess)
-      return fail(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
-    // an ordinary launch: earlier work of the stream may be writing the inputs
-    mla::mla_page_score_kernel<<<dim3(mla::ceil_div(max_pages, mla::kScorePages), pairs),
-                                 mla::kScoreThreads, mla::kScoreSmem, st>>>(p);
-    MLA_CUDA(cudaGetLastError());
-    PdlLaunch L(dim3(pairs), dim3(mla::kSelectThreads), 0, st);
-    MLA_CUDA(cudaLaunchKernelEx(&L.cfg, mla::mla_page_select_kernel, p));
-  } else {
-    mla::mla_page_select_kernel<<<pairs, mla::kSelectThreads, 0, st>>>(p);
-    MLA_CUDA(cudaGetLastError());
-  }
-  if ((rc = mla_get_metadata(lens, pairs, h_q, 1, num_sm_parts, meta, splits, stream)) != MLA_OK)
-    return rc;
+  p.num_parts = num_sm_parts;
+  p.plan = mla::plan_params(h_q);
+  p.metadata = meta;
+  p.num_splits = splits;
+  MLA_CUDA(allow_smem<mla::mla_page_select_kernel>(mla::select_smem(mla::kSelHeads, 0)));
+  // CTAs per pair: as many as there are tiles of pages to score, while all of
+  // them still run at once (one per SM)
+  int dev = 0, sms = 0;
+  MLA_CUDA(cudaGetDevice(&dev));
+  MLA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  int cluster = 1;
+  if (topk_pages < max_pages)
+    while (cluster < mla::kSelMaxCluster && 2 * cluster * (pairs + 1) <= sms &&
+           cluster * mla::kSelTile < max_pages)
+      cluster *= 2;
+  // an ordinary launch: earlier work of the stream may be writing the inputs
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(pairs + 1));
+  cfg.blockDim = dim3(mla::kSelThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(mla::select_smem(h_q, pairs));
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_page_select_kernel, p));
   return mla_decode_fwd(q, kcache, table, w.width, num_blocks, lens, pairs, 1, h_q, 1, d_v,
                         softmax_scale, 0, meta, splits, num_sm_parts, ws + w.dense_off,
                         w.dense_bytes, out, lse, stream);

@@ -34,10 +34,6 @@ __device__ __forceinline__ int int8_code(float x, float scale) {
   return max(-127, min(127, c));
 }
 
-__device__ __forceinline__ uint32_t pack_int8x4(int a, int b, int c, int d) {
-  return (a & 0xFF) | ((b & 0xFF) << 8) | ((c & 0xFF) << 16) | (static_cast<uint32_t>(d) << 24);
-}
-
 // ------------------------------------------------------------------ page keys
 
 struct PageKeysParams {
@@ -120,7 +116,7 @@ __global__ void __launch_bounds__(kKeyThreads) mla_page_keys_kernel(const PageKe
   if (threadIdx.x == 0) P.scales[blk] = scale;
 }
 
-// ------------------------------------------------------------------ scores
+// ------------------------------------------------------------------ selection
 
 struct PageSelectParams {
   const __nv_bfloat16* q;  // [pairs * h_q, 576]
@@ -130,31 +126,51 @@ struct PageSelectParams {
   const int32_t* block_table;
   int max_pages;
   const int32_t* seqlens;  // [batch]
-  int s_q, h_q, causal;
+  int pairs, s_q, h_q, causal;
   int topk;                // pages taken (at most)
   int width;               // pages of a taken table row: min(topk, max_pages)
-  float* scores;           // [pairs, max_pages]
+  uint32_t* scores;        // [pairs, max_pages] order keys >= 1 (scores while heads are left)
   int32_t* taken_table;    // [pairs, width] physical blocks
   int32_t* taken_lens;     // [pairs]
   int32_t* pages;          // [pairs, topk] logical pages, -1 behind them; or null
+  // the plan of the decode over the taken pages
+  int num_parts;
+  PlanParams plan;
+  int32_t* metadata;
+  int32_t* num_splits;
 };
 
 // Tokens that query `pair` sees (0 .. max_pages * 64).
 __device__ __forceinline__ int tokens_seen(const PageSelectParams& P, int pair) {
   const int b = pair / P.s_q, i = pair - b * P.s_q;
-  int L = P.seqlens[b];
-  if (L > P.max_pages * kPage) {
-    if (threadIdx.x == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x73);
-    L = P.max_pages * kPage;
-  }
+  const int L = max(0, min(P.seqlens[b], P.max_pages * kPage));
   return max(0, P.causal ? L - P.s_q + 1 + i : L);
 }
 
-constexpr int kScorePages = 128;   // pages per CTA
-constexpr int kScoreHeads = 64;    // head rows per pass
-constexpr int kScoreThreads = 256;
-constexpr int kScoreStride = kD + 16;  // bytes; an odd number of 16-byte units: no bank conflicts
-constexpr int kScoreSmem = (kScorePages + kScoreHeads) * kScoreStride;
+// Tokens of the pages taken for a query that sees `seen` tokens: known before
+// the selection, since the last page is always among them.
+__device__ __forceinline__ int taken_tokens(const PageSelectParams& P, int seen) {
+  const int last = (seen + kPage - 1) / kPage - 1;
+  return last < P.topk ? seen : (P.topk - 1) * kPage + seen - last * kPage;
+}
+
+constexpr int kSelThreads = 512;
+constexpr int kSelTile = 64;     // pages per step of a CTA
+constexpr int kSelHeads = 128;   // head rows per pass
+constexpr int kSelStride = kD + 16;  // bytes; an odd number of 16-byte units: no bank conflicts
+constexpr int kSelPerThread = 8;     // order keys a thread of the selection keeps in registers
+constexpr int kSelMaxCluster = 8;
+
+// Head rows that a pass of `h_q` heads holds (the warps take 32 at a time).
+__host__ __device__ inline int select_rows(int h_q) {
+  return h_q >= kSelHeads ? kSelHeads : (h_q + 31) / 32 * 32;
+}
+// Dynamic shared memory: the rows' codes and two tiles of keys, or the plan's
+// prefix sums of pairs + 1 costs.
+__host__ __device__ inline int select_smem(int h_q, int pairs) {
+  const int a = (select_rows(h_q) + 2 * kSelTile) * kSelStride, b = (pairs + 1) * 4;
+  return a > b ? a : b;
+}
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -171,149 +187,18 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// grid (ceil(max_pages / 128), pairs).  A CTA quantises the pair's query rows
-// (64 heads at a time), multiplies them with its pages' keys on the integer
-// tensor cores (warp tile 32 heads x 32 pages) and keeps each page's maximum.
-// The keys are 576 bytes a page, 1/128 of the rows they stand for, so the whole
-// step is bound by its latency and the quantisation, not by bytes.
-__global__ void __launch_bounds__(kScoreThreads, 2) mla_page_score_kernel(const PageSelectParams P) {
-  extern __shared__ __align__(16) uint8_t s_buf[];
-  __shared__ float s_qscale[kScoreHeads];
-  __shared__ float s_best[2][kScorePages];  // [head half][page]
-  ptx::grid_dep_launch();
-  const int pair = blockIdx.y;
-  const int page0 = blockIdx.x * kScorePages;
-  const int seen = tokens_seen(P, pair);
-  const int last = (seen + kPage - 1) / kPage - 1;
-  // nothing to choose, or no page before the last one here
-  if (last < P.topk || page0 >= last) return;
-  uint8_t* s_keys = s_buf;
-  uint8_t* s_q = s_buf + kScorePages * kScoreStride;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t* table = P.block_table + static_cast<size_t>(pair / P.s_q) * P.max_pages;
-
-  // the pages' keys: 36 16-byte units each
-  for (int i = tid; i < kScorePages * (kD / 16); i += kScoreThreads) {
-    const int p = i / (kD / 16), c = i - p * (kD / 16);
-    uint8_t* dst = s_keys + p * kScoreStride + 16 * c;
-    if (page0 + p < last) {
-      const int blk = clamp_block(table[page0 + p], P.num_blocks);
-      const int8_t* src = P.keys + static_cast<size_t>(blk) * kD + 16 * c;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src));
-    } else {
-      *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
-    }
-  }
-  asm volatile("cp.async.commit_group;");
-  if (tid < kScorePages) s_best[0][tid] = s_best[1][tid] = -INFINITY;
-
-  const int hh = warp >> 2;  // head half: rows 32 hh .. + 31
-  const int pg = warp & 3;   // pages 32 pg .. + 31
-  for (int h0 = 0; h0 < P.h_q; h0 += kScoreHeads) {
-    __syncthreads();  // the previous pass is done with s_q
-    for (int r = warp; r < kScoreHeads; r += kScoreThreads / 32) {
-      uint8_t* dst = s_q + r * kScoreStride;
-      if (h0 + r >= P.h_q) {
-        for (int u = lane; u < kD / 8; u += 32)
-          *reinterpret_cast<uint2*>(dst + 8 * u) = make_uint2(0, 0);
-        continue;
-      }
-      const uint4* src = reinterpret_cast<const uint4*>(
-          P.q + (static_cast<size_t>(pair) * P.h_q + h0 + r) * kD);
-      float x[3][8];
-      float amax = 0.f;
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const int u = lane + 32 * j;
-        const uint4 w = u < kD / 8 ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[j][2 * e] = __uint_as_float(v[e] << 16);
-          x[j][2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
-          amax = fmaxf(amax, fmaxf(fabsf(x[j][2 * e]), fabsf(x[j][2 * e + 1])));
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const float scale = int8_scale(amax);
-      if (lane == 0) s_qscale[r] = scale;
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const int u = lane + 32 * j;
-        int c[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = int8_code(x[j][e], scale);
-        if (u < kD / 8)
-          *reinterpret_cast<uint2*>(dst + 8 * u) =
-              make_uint2(pack_int8x4(c[0], c[1], c[2], c[3]), pack_int8x4(c[4], c[5], c[6], c[7]));
-      }
-    }
-    if (h0 == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-
-    if (h0 + 32 * hh < P.h_q) {
-      int acc[2][4][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][n][e] = 0;
-      // ldmatrix rows: A tiles (16 heads x 32 bytes) and B tiles (16 pages x 32 bytes)
-      const uint32_t a0 = ptx::smem_u32(s_q) + (32 * hh + (lane & 15)) * kScoreStride +
-                          16 * (lane >> 4);
-      const uint32_t b0 = ptx::smem_u32(s_keys) +
-                          (32 * pg + (lane & 7) + 8 * (lane >> 4)) * kScoreStride +
-                          16 * ((lane >> 3) & 1);
-#pragma unroll
-      for (int k = 0; k < kD / 32; ++k) {
-        uint32_t a[2][4], bq[2][4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) ldmatrix_x4(a[m], a0 + 16 * m * kScoreStride + 32 * k);
-#pragma unroll
-        for (int n = 0; n < 2; ++n) ldmatrix_x4(bq[n], b0 + 16 * n * kScoreStride + 32 * k);
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-            mma_s8(acc[m][n], a[m], bq[n >> 1][2 * (n & 1)], bq[n >> 1][2 * (n & 1) + 1]);
-      }
-      // max over the warp's 32 heads of s_h * dot, per page
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = -INFINITY;
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int hi = 0; hi < 2; ++hi) {
-              const int r = 32 * hh + 16 * m + 8 * hi + (lane >> 2);
-              if (h0 + r < P.h_q)
-                v = fmaxf(v, static_cast<float>(acc[m][n][2 * hi + e]) * s_qscale[r]);
-            }
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-          if (lane < 4) {
-            float& best = s_best[hh][32 * pg + 8 * n + 2 * lane + e];
-            best = fmaxf(best, v);
-          }
-        }
-    }
-  }
-  __syncthreads();
-  if (tid < kScorePages && page0 + tid < last) {
-    const int blk = clamp_block(table[page0 + tid], P.num_blocks);
-    // + 0: a product that underflows to -0 ties with 0
-    P.scores[static_cast<size_t>(pair) * P.max_pages + page0 + tid] =
-        fmaxf(s_best[0][tid], s_best[1][tid]) * P.scales[blk] + 0.f;
-  }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-
-// ------------------------------------------------------------------ selection
-
-constexpr int kSelectThreads = 256;
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
 
 // fp32 -> unsigned key of the same order.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -321,100 +206,316 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// grid (pairs): one CTA finds the (topk - 1)-th highest score by a radix
-// selection (four passes of eight bits), then takes the pages above it and the
-// first of those equal to it, in page order.
-__global__ void __launch_bounds__(kSelectThreads) mla_page_select_kernel(const PageSelectParams P) {
+// int8_code of eight values.  x * (1/scale) is within 2e-5 of x / scale (two
+// roundings of a value of at most 127), so its nearest whole number is the
+// quotient's unless it lies within 1e-4 of a half; those, and scales whose
+// reciprocal is not a normal number, take the division.  The whole number
+// comes from adding 1.5 * 2^23, in whose unit it then is the low byte.
+__device__ __forceinline__ uint2 int8_codes8(const float* x, float scale, float inv, bool plain) {
+  constexpr float kMagic = 12582912.f;
+  uint32_t m[8];
+  bool near_half = plain;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float y = x[e] * inv;
+    const float r = y + kMagic;
+    m[e] = __float_as_uint(r);
+    near_half |= !(fabsf(y - (r - kMagic)) < 0.4999f);  // true for NaN
+  }
+  if (near_half) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[e] = static_cast<uint32_t>(int8_code(x[e], scale));
+  }
+  uint2 o;
+  o.x = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
+  o.y = __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410);
+  return o;
+}
+
+// grid (cluster, 1 + pairs).  Row 0 of the grid: one CTA plans the decode over
+// the taken pages, whose lengths do not depend on the selection.  Row 1 + pair:
+// a cluster of 1..8 CTAs scores the pair's pages and its first CTA selects.
+//   - Each CTA quantises its share of the head rows (128 at a time) and stores
+//     the codes to every CTA of the cluster through distributed shared memory.
+//   - Tiles of 64 pages go round the CTAs.  A tile's keys (37 kB) come in by
+//     cp.async, the next tile's behind this one's products; 4 x 4 warps take
+//     32 heads x 16 pages each on the integer tensor cores, and the maximum
+//     over the heads goes to the score array as an order key.
+//   - The first CTA finds the border, the (topk - 1)-th highest key, bit by bit
+//     with the keys in registers, and takes the pages above it and the first of
+//     those equal to it, in page order.
+// The keys are 576 bytes a page, 1/128 of the rows they stand for: latency, not
+// bytes, bounds this step, hence one launch for plan, scores and selection.
+__global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const PageSelectParams P) {
+  extern __shared__ __align__(16) uint8_t s_buf[];
+  __shared__ float s_qscale[kSelHeads];
+  __shared__ float s_best[4][kSelTile];  // [head quarter][page]
+  __shared__ int s_count[2][kSelThreads / 32];
   __shared__ int s_hist[256];
-  __shared__ int s_warp[kSelectThreads / 32][2];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  ptx::grid_dep_wait();  // the scores are complete
-  ptx::grid_dep_launch();
-  const int pair = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x, nrank = gridDim.x;
+  ptx::grid_dep_launch();  // the decode grid waits for this one's end
+  if (blockIdx.y == 0) {
+    if (rank == 0)
+      plan_block<kSelThreads>([&](int pair) { return taken_tokens(P, tokens_seen(P, pair)); },
+                              P.pairs, P.num_parts, P.plan, reinterpret_cast<int32_t*>(s_buf),
+                              P.metadata, P.num_splits, nullptr, nullptr, 0);
+    return;
+  }
+  const int pair = blockIdx.y - 1;
   const int seen = tokens_seen(P, pair);
   const int last = (seen + kPage - 1) / kPage - 1;  // -1: the query sees nothing
   const int32_t* table = P.block_table + static_cast<size_t>(pair / P.s_q) * P.max_pages;
+  uint32_t* scores = P.scores + static_cast<size_t>(pair) * P.max_pages;
+  const bool choose = last >= P.topk && P.topk > 1;  // alike in the whole cluster
+
+  if (choose) {
+    cluster_arrive();  // this CTA runs: the others may store to its shared memory
+    const int rows = select_rows(P.h_q);
+    uint8_t* s_q = s_buf;
+    uint8_t* s_keys = s_buf + rows * kSelStride;
+    const int tiles = (last + kSelTile - 1) / kSelTile;
+    // a tile's keys: eight threads a page, 36 units of 16 bytes
+    auto load_tile = [&](int t, int buf) {
+      const int p = t * kSelTile + (tid >> 3);
+      if (t < tiles && p < last) {
+        const int blk = clamp_block(table[p], P.num_blocks);
+        const int8_t* src = P.keys + static_cast<size_t>(blk) * kD;
+        const uint32_t dst = ptx::smem_u32(s_keys) + (buf * kSelTile + (tid >> 3)) * kSelStride;
+        for (int u = tid & 7; u < kD / 16; u += 8)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * u),
+                       "l"(src + 16 * u)
+                       : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int h0 = 0; h0 < P.h_q; h0 += kSelHeads) {
+      load_tile(rank, 0);
+      if (h0 > 0) cluster_arrive();  // the previous pass is done with the codes
+      bool stored = false;
+      const int nh = min(kSelHeads, P.h_q - h0);
+      for (int r = rank + nrank * warp; r < nh; r += nrank * (kSelThreads / 32)) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            P.q + (static_cast<size_t>(pair) * P.h_q + h0 + r) * kD);
+        uint4 w[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const int u = lane + 32 * j;
+          w[j] = u < kD / 8 ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+        }
+        float x[3][8];
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const uint32_t v[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[j][2 * e] = __uint_as_float(v[e] << 16);
+            x[j][2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
+            amax = fmaxf(amax, fmaxf(fabsf(x[j][2 * e]), fabsf(x[j][2 * e + 1])));
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float scale = int8_scale(amax);
+        const bool plain = !(scale > 0x1p-100f && scale < 0x1p+100f);
+        const float inv = plain ? 0.f : 1.f / scale;
+        uint2 code[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) code[j] = int8_codes8(x[j], scale, inv, plain);
+        if (!stored) {
+          __syncwarp();
+          cluster_wait();
+          stored = true;
+        }
+        const uint32_t dst = ptx::smem_u32(s_q) + r * kSelStride;
+        for (int c = 0; c < nrank; ++c) {
+          const uint32_t to = ptx::mapa_shared(dst, c);
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            if (lane + 32 * j < kD / 8) st_cluster_v2(to + 8 * (lane + 32 * j), code[j].x, code[j].y);
+          if (lane == 0) st_cluster(ptx::mapa_shared(ptx::smem_u32(&s_qscale[r]), c), scale);
+        }
+      }
+      if (!stored) cluster_wait();
+      cluster_arrive();  // this warp's codes are stored
+      cluster_wait();
+
+      const int hq4 = warp >> 2;  // heads 32 hq4 .. + 31
+      const int pg = warp & 3;    // pages 16 pg .. + 15 of the tile
+      const bool final_pass = h0 + kSelHeads >= P.h_q;
+      for (int t = rank, i = 0; t < tiles; t += nrank, ++i) {
+        load_tile(t + nrank, (i + 1) & 1);
+        const int p = t * kSelTile + tid;
+        float key_scale = 0.f, prev = -INFINITY;
+        if (tid < kSelTile && p < last) {
+          key_scale = P.scales[clamp_block(table[p], P.num_blocks)];
+          if (h0 > 0) prev = __uint_as_float(scores[p]);
+        }
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();  // the tile's keys are in shared memory
+        if (32 * hq4 < nh) {
+          int acc[2][2][4];
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[m][n][e] = 0;
+          // ldmatrix rows: A tiles (16 heads x 32 bytes) and a B tile (16 pages x 32 bytes)
+          const uint32_t a0 = ptx::smem_u32(s_q) + (32 * hq4 + (lane & 15)) * kSelStride +
+                              16 * (lane >> 4);
+          const uint32_t b0 = ptx::smem_u32(s_keys) +
+                              ((i & 1) * kSelTile + 16 * pg + (lane & 7) + 8 * (lane >> 4)) *
+                                  kSelStride +
+                              16 * ((lane >> 3) & 1);
+#pragma unroll 6
+          for (int k = 0; k < kD / 32; ++k) {
+            uint32_t a[2][4], bq[4];
+            ldmatrix_x4(bq, b0 + 32 * k);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) ldmatrix_x4(a[m], a0 + 16 * m * kSelStride + 32 * k);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int n = 0; n < 2; ++n) mma_s8(acc[m][n], a[m], bq[2 * n], bq[2 * n + 1]);
+          }
+          // max over the warp's 32 heads of s_h * dot, per page
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float v = -INFINITY;
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                  const int r = 32 * hq4 + 16 * m + 8 * hi + (lane >> 2);
+                  if (r < nh) v = fmaxf(v, static_cast<float>(acc[m][n][2 * hi + e]) * s_qscale[r]);
+                }
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+              if (lane < 4) s_best[hq4][16 * pg + 8 * n + 2 * lane + e] = v;
+            }
+        }
+        __syncthreads();  // s_best is complete, the tile's buffer free
+        if (tid < kSelTile && p < last) {
+          float v = prev;
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            if (32 * g < nh) v = fmaxf(v, s_best[g][tid]);
+          // + 0: a product that underflows to -0 ties with 0
+          scores[p] = final_pass ? max(order_key(v * key_scale + 0.f), 1u) : __float_as_uint(v);
+        }
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    cluster_arrive();  // this CTA's scores are written
+    cluster_wait();
+  }
+  if (rank != 0) return;
+
+  if (tid == 0 && P.seqlens[pair / P.s_q] > P.max_pages * kPage)
+    ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x73);
   int32_t* out_table = P.taken_table + static_cast<size_t>(pair) * P.width;
   int32_t* out_pages = P.pages ? P.pages + static_cast<size_t>(pair) * P.topk : nullptr;
   auto take = [&](int at, int page) {
     out_table[at] = clamp_block(table[page], P.num_blocks);
     if (out_pages) out_pages[at] = page;
   };
-  int count = last + 1;  // pages taken
-  if (last < P.topk) {
-    for (int p = tid; p <= last; p += kSelectThreads) take(p, p);
-  } else {
-    count = P.topk;
-    const float* scores = P.scores + static_cast<size_t>(pair) * P.max_pages;
-    uint32_t prefix = 0;
-    int need = P.topk - 1;  // still to take among the pages that share `prefix`
-    for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-      s_hist[tid] = 0;
-      __syncthreads();
-      for (int p = tid; p < last; p += kSelectThreads) {
-        const uint32_t key = order_key(scores[p]);
-        if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&s_hist[(key >> shift) & 255u], 1);
-      }
-      __syncthreads();
-      // suffix sums: thread d holds the count of digits above 255 - d
-      const int d = 255 - tid;
-      const int mine = s_hist[d];
-      int x = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) s_warp[warp][0] = x;
-      __syncthreads();
-      for (int w = 0; w < warp; ++w) x += s_warp[w][0];
-      const int above = x - mine;
-      if (above < need && need <= x) {  // exactly one digit
-        s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
-        s_need = need - above;
-      }
-      __syncthreads();
-      prefix = s_prefix;
-      need = s_need;
-    }
-    // prefix is the border's key (no border when only the last page is taken);
-    // `need` pages of that key are taken
-    int gt0 = 0, eq0 = 0;
-    for (int base = 0; base < last; base += kSelectThreads) {
-      const int p = base + tid;
-      bool gt = false, eq = false;
-      if (p < last && P.topk > 1) {
-        const uint32_t key = order_key(scores[p]);
-        gt = key > prefix;
-        eq = key == prefix;
-      }
-      const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-      __syncthreads();  // s_warp of the previous chunk was read
-      if (lane == 0) {
-        s_warp[warp][0] = __popc(bg);
-        s_warp[warp][1] = __popc(be);
-      }
-      __syncthreads();
-      const uint32_t below = (1u << lane) - 1u;
-      int g = gt0 + __popc(bg & below), q = eq0 + __popc(be & below);
-      for (int w = 0; w < kSelectThreads / 32; ++w) {
-        if (w < warp) {
-          g += s_warp[w][0];
-          q += s_warp[w][1];
-        }
-        gt0 += s_warp[w][0];
-        eq0 += s_warp[w][1];
-      }
-      if (gt || (eq && q < need)) take(g + min(q, need), p);
-    }
-    if (tid == 0) take(P.topk - 1, last);
-  }
+  const int count = min(last + 1, P.topk);  // pages taken
+  if (tid == 0) P.taken_lens[pair] = taken_tokens(P, seen);
   if (out_pages)
-    for (int p = count + tid; p < P.topk; p += kSelectThreads) out_pages[p] = -1;
-  if (tid == 0) P.taken_lens[pair] = last < 0 ? 0 : (count - 1) * kPage + seen - last * kPage;
+    for (int p = count + tid; p < P.topk; p += kSelThreads) out_pages[p] = -1;
+  if (last < P.topk) {
+    for (int p = tid; p <= last; p += kSelThreads) take(p, p);
+    return;
+  }
+  if (tid == 0) take(P.topk - 1, last);
+  if (!choose) return;
+  int need = P.topk - 1;  // pages to take before the last one
+  if (last <= kSelThreads * kSelPerThread) {
+    // thread t keeps the keys of pages n t .. n t + n - 1; border: the highest T
+    // with at least `need` keys >= T, found from its top bit down, or the first
+    // T on the way with exactly `need`
+    const int n = (last + kSelThreads - 1) / kSelThreads;
+    uint32_t key[kSelPerThread];
+#pragma unroll
+    for (int k = 0; k < kSelPerThread; ++k)
+      key[k] = k < n && n * tid + k < last ? __ldcg(scores + n * tid + k) : 0u;  // 0: no page
+    uint32_t border = 0;
+    int at_least = -1;  // keys >= border
+    for (int bit = 31; bit >= 0 && at_least != need; --bit) {
+      const uint32_t probe = border | (1u << bit);
+      int c = 0;
+#pragma unroll
+      for (int k = 0; k < kSelPerThread; ++k) c += key[k] >= probe;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) s_count[bit & 1][warp] = c;
+      __syncthreads();  // the other half of s_count is written next
+      c = __reduce_add_sync(0xffffffffu, lane < kSelThreads / 32 ? s_count[bit & 1][lane] : 0);
+      if (c >= need) {
+        border = probe;
+        at_least = c;
+      }
+    }
+    int above = 0, equal = 0;
+#pragma unroll
+    for (int k = 0; k < kSelPerThread; ++k) {
+      above += key[k] > border;
+      equal += key[k] == border;
+    }
+    int total;
+    const int before = block_exclusive_scan<kSelThreads>(above | (equal << 16), &total);
+    need -= total & 0xFFFF;  // of the keys equal to the border
+    int g = before & 0xFFFF, q = before >> 16;
+#pragma unroll
+    for (int k = 0; k < kSelPerThread; ++k) {
+      const bool eq = key[k] == border;
+      if (key[k] > border || (eq && q < need)) take(g + min(q, need), n * tid + k);
+      g += key[k] > border;
+      q += eq;
+    }
+    return;
+  }
+  // more pages than the registers hold: radix selection of the border, four
+  // passes of eight bits over the score array, then chunks in page order
+  uint32_t prefix = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (tid < 256) s_hist[tid] = 0;
+    __syncthreads();
+    for (int p = tid; p < last; p += kSelThreads) {
+      const uint32_t key = __ldcg(scores + p);
+      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
+        atomicAdd(&s_hist[(key >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    // thread d < 256: keys of the digits above and of digit 255 - d
+    const int d = 255 - tid;
+    const int mine = tid < 256 ? s_hist[d] : 0;
+    int total;
+    const int above = block_exclusive_scan<kSelThreads>(mine, &total);
+    if (tid < 256 && above < need && need <= above + mine) {  // exactly one digit
+      s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
+      s_need = need - above;
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    need = s_need;
+  }
+  int gt0 = 0, eq0 = 0;
+  for (int base = 0; base < last; base += kSelThreads) {
+    const uint32_t key = base + tid < last ? __ldcg(scores + base + tid) : 0u;
+    const int gt = key > prefix, eq = key == prefix;
+    int total;
+    const int before = block_exclusive_scan<kSelThreads>(gt | (eq << 16), &total);
+    const int g = gt0 + (before & 0xFFFF), q = eq0 + (before >> 16);
+    if (gt || (eq && q < need)) take(g + min(q, need), base + tid);
+    gt0 += total & 0xFFFF;
+    eq0 += total >> 16;
+  }
 }
 
 }  // namespace mla

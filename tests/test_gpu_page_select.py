@@ -237,6 +237,18 @@ def test_many_pages_and_chunks():
         c.check(c.run(topk), topk)
 
 
+@pytest.mark.parametrize("h_q", [16, 200])
+@pytest.mark.parametrize("pages", [512, 513, 4096, 4097, 6001])
+def test_long_tables(pages, h_q):
+    # pages of few blocks: many equal scores, and tables beyond one chunk of the selection
+    c = Case([64 * 300], h_q=h_q, seed=pages)
+    g = torch.Generator().manual_seed(pages)
+    c.lengths = [64 * pages + 5]
+    c.table = torch.randint(0, 300, (1, pages + 1), generator=g).to(torch.int32)
+    for topk in (2, 33, 500):
+        c.check(c.run(topk), topk)
+
+
 def test_d_v_576():
     c = Case([700, 100], seed=8, d_v=576)
     c.check(c.run(4), 4)
