@@ -158,12 +158,12 @@ constexpr int kSelThreads = 512;
 constexpr int kSelTile = 64;     // pages per step of a CTA
 constexpr int kSelHeads = 128;   // head rows per pass
 constexpr int kSelStride = kD + 16;  // bytes; an odd number of 16-byte units: no bank conflicts
-constexpr int kSelPerThread = 8;     // order keys a thread of the selection keeps in registers
+constexpr int kSelPerThread = 8;     // order keys a thread of the selection holds, at most
 constexpr int kSelMaxCluster = 8;
 
-// Head rows that a pass of `h_q` heads holds (the warps take 32 at a time).
+// Head rows that a pass of `h_q` heads holds (a warp takes 16).
 __host__ __device__ inline int select_rows(int h_q) {
-  return h_q >= kSelHeads ? kSelHeads : (h_q + 31) / 32 * 32;
+  return h_q >= kSelHeads ? kSelHeads : (h_q + 15) / 16 * 16;
 }
 // Dynamic shared memory: the rows' codes and two tiles of keys, or the plan's
 // prefix sums of pairs + 1 costs.
@@ -206,30 +206,109 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// int8_code of eight values.  x * (1/scale) is within 2e-5 of x / scale (two
-// roundings of a value of at most 127), so its nearest whole number is the
-// quotient's unless it lies within 1e-4 of a half; those, and scales whose
-// reciprocal is not a normal number, take the division.  The whole number
-// comes from adding 1.5 * 2^23, in whose unit it then is the low byte.
-__device__ __forceinline__ uint2 int8_codes8(const float* x, float scale, float inv, bool plain) {
+// Eight codes by division, for scales whose reciprocal is not a normal number.
+// Hardly ever taken: kept out of line and out of the instruction cache.
+__device__ __noinline__ uint2 int8_codes8_by_division(float4 lo, float4 hi, float scale) {
+  const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t o[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e >> 2] |= (int8_code(x[e], scale) & 0xFF) << (8 * (e & 3));
+  return make_uint2(o[0], o[1]);
+}
+
+// int8_code of eight finite values, inv = 1/scale correctly rounded: one step
+// from q = x inv, q + (x - q scale) inv, is then the correctly rounded quotient
+// (Markstein, IBM J. Res. Dev. 34, 1990).  Adding 1.5 * 2^23 rounds it to a
+// whole number, ties to even, whose low byte is the code.
+__device__ __forceinline__ uint2 int8_codes8(const float* x, float scale, float inv) {
   constexpr float kMagic = 12582912.f;
   uint32_t m[8];
-  bool near_half = plain;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float y = x[e] * inv;
-    const float r = y + kMagic;
-    m[e] = __float_as_uint(r);
-    near_half |= !(fabsf(y - (r - kMagic)) < 0.4999f);  // true for NaN
-  }
-  if (near_half) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m[e] = static_cast<uint32_t>(int8_code(x[e], scale));
+    const float q = __fmul_rn(x[e], inv);
+    m[e] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-q, scale, x[e]), inv, q), kMagic));
   }
   uint2 o;
   o.x = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
   o.y = __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410);
   return o;
+}
+
+// Selection by one CTA, thread t holding the keys of pages m t .. m t + m - 1
+// (m = ceil(n / threads) <= kKeys).  The border is the highest T with at least
+// `need` keys >= T, found two bits a round from the highest bit in which the
+// keys differ, or the first T on the way with exactly `need`.  take(i, page,
+// entry): the i-th page, in page order, of the keys above the border and the
+// first of those equal to it, with the page's block table entry.
+template <int kKeys, class Take>
+__device__ __forceinline__ void select_block(const uint32_t* keys, const int32_t* table, int n,
+                                             int need, Take take) {
+  constexpr int kWarps = kSelThreads / 32;
+  __shared__ uint32_t s_part[2][2][kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int m = (n + kSelThreads - 1) / kSelThreads;
+  uint32_t key[kKeys];
+  int entry[kKeys];
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {  // unconditional: all loads are in flight at once
+    const int p = min(m * tid + k, n - 1);
+    key[k] = __ldcg(keys + p);
+    entry[k] = __ldg(table + p);
+  }
+  uint32_t top = 0, low = 0xffffffffu;
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    top = max(top, key[k]);
+    low = min(low, key[k]);
+    if (k >= m || m * tid + k >= n) key[k] = 0u;  // no page
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) {
+    s_part[1][0][warp] = top;
+    s_part[1][1][warp] = low;
+  }
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, s_part[1][0][lane & (kWarps - 1)]);
+  low = __reduce_min_sync(0xffffffffu, s_part[1][1][lane & (kWarps - 1)]);
+  // keys >= border: n at the start, where the border holds the common bits
+  int bit = top == low ? -1 : (31 - __clz(top ^ low)) | 1;  // the upper of two bits
+  uint32_t border = bit < 0 ? top : bit == 31 ? 0u : top & ~((2u << bit) - 1u);
+  int count = n;
+#pragma unroll 1
+  for (int round = 0; bit > 0 && count != need; bit -= 2, round ^= 1) {
+    const uint32_t step = 1u << (bit - 1);
+    uint32_t c = 0;  // three counts of at most 32 kKeys
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k)
+      c += (key[k] >= border + step ? 1u : 0u) + (key[k] >= border + 2 * step ? 1u << 10 : 0u) +
+           (key[k] >= border + 3 * step ? 1u << 20 : 0u);
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) s_part[round][0][warp] = c;
+    __syncthreads();  // the other half of s_part is written next
+    c = lane < kWarps ? s_part[round][0][lane] : 0u;
+    const uint32_t c12 = __reduce_add_sync(0xffffffffu, (c & 1023u) | (c >> 10 & 1023u) << 16);
+    const int c3 = __reduce_add_sync(0xffffffffu, c >> 20);
+    const int c1 = c12 & 0xFFFFu, c2 = c12 >> 16;
+    const int up = c3 >= need ? 3 : c2 >= need ? 2 : c1 >= need ? 1 : 0;
+    border += up * step;
+    count = up == 3 ? c3 : up == 2 ? c2 : up == 1 ? c1 : count;
+  }
+  int mine = 0;  // keys above, and equal to, the border
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k)
+    mine += (key[k] > border ? 1 : 0) + (key[k] == border ? 1 << 16 : 0);
+  int total;
+  const int before = block_exclusive_scan<kSelThreads>(mine, &total);
+  const int equal = need - (total & 0xFFFF);  // taken of those equal to the border
+  int g = before & 0xFFFF, q = before >> 16;
+#pragma unroll
+  for (int k = 0; k < kKeys; ++k) {
+    const bool gt = key[k] > border, eq = key[k] == border;
+    if (gt || (eq && q < equal)) take(g + min(q, equal), m * tid + k, entry[k]);
+    g += gt;
+    q += eq;
+  }
 }
 
 // grid (cluster, 1 + pairs).  Row 0 of the grid: one CTA plans the decode over
@@ -238,19 +317,18 @@ __device__ __forceinline__ uint2 int8_codes8(const float* x, float scale, float 
 //   - Each CTA quantises its share of the head rows (128 at a time) and stores
 //     the codes to every CTA of the cluster through distributed shared memory.
 //   - Tiles of 64 pages go round the CTAs.  A tile's keys (37 kB) come in by
-//     cp.async, the next tile's behind this one's products; 4 x 4 warps take
-//     32 heads x 16 pages each on the integer tensor cores, and the maximum
-//     over the heads goes to the score array as an order key.
-//   - The first CTA finds the border, the (topk - 1)-th highest key, bit by bit
-//     with the keys in registers, and takes the pages above it and the first of
-//     those equal to it, in page order.
+//     cp.async, the next tile's behind this one's products.  A warp keeps the
+//     codes of 16 heads in registers as the A operand and multiplies them with
+//     16 or 32 pages of the tile on the integer tensor cores; the maximum over
+//     the heads goes to the score array as an order key.
+//   - The first CTA selects.
 // The keys are 576 bytes a page, 1/128 of the rows they stand for: latency, not
-// bytes, bounds this step, hence one launch for plan, scores and selection.
+// bytes, bounds this step, hence one launch for plan, scores and selection, and
+// the query, the table and the length read side by side at its start.
 __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const PageSelectParams P) {
   extern __shared__ __align__(16) uint8_t s_buf[];
   __shared__ float s_qscale[kSelHeads];
-  __shared__ float s_best[4][kSelTile];  // [head quarter][page]
-  __shared__ int s_count[2][kSelThreads / 32];
+  __shared__ float s_best[kSelHeads / 16][kSelTile];  // [16 heads][page]
   __shared__ int s_hist[256];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
@@ -265,10 +343,29 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
     return;
   }
   const int pair = blockIdx.y - 1;
-  const int seen = tokens_seen(P, pair);
-  const int last = (seen + kPage - 1) / kPage - 1;  // -1: the query sees nothing
   const int32_t* table = P.block_table + static_cast<size_t>(pair / P.s_q) * P.max_pages;
   uint32_t* scores = P.scores + static_cast<size_t>(pair) * P.max_pages;
+  // raw values of one head row: lane l holds the 16-byte units l, l + 32, l + 64
+  auto load_row = [&](int h, uint4 (&w)[3]) {
+    const uint4* src =
+        reinterpret_cast<const uint4*>(P.q + (static_cast<size_t>(pair) * P.h_q + h) * kD);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const int u = lane + 32 * j;
+      w[j] = u < kD / 8 ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  const int row0 = rank + nrank * warp, row_step = nrank * (kSelThreads / 32);
+  const int page_of_thread = tid >> 3;  // of a tile: eight threads load a page's key
+  uint4 raw[3];
+  int entry = 0;  // the table's entry of the first tile's page
+  if (P.topk > 1 && P.topk < P.max_pages) {
+    if (row0 < min(kSelHeads, P.h_q)) load_row(row0, raw);
+    if (rank * kSelTile + page_of_thread < P.max_pages)
+      entry = table[rank * kSelTile + page_of_thread];
+  }
+  const int seen = tokens_seen(P, pair);
+  const int last = (seen + kPage - 1) / kPage - 1;  // -1: the query sees nothing
   const bool choose = last >= P.topk && P.topk > 1;  // alike in the whole cluster
 
   if (choose) {
@@ -277,13 +374,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
     uint8_t* s_q = s_buf;
     uint8_t* s_keys = s_buf + rows * kSelStride;
     const int tiles = (last + kSelTile - 1) / kSelTile;
-    // a tile's keys: eight threads a page, 36 units of 16 bytes
-    auto load_tile = [&](int t, int buf) {
-      const int p = t * kSelTile + (tid >> 3);
-      if (t < tiles && p < last) {
-        const int blk = clamp_block(table[p], P.num_blocks);
+    // a tile's keys, 36 units of 16 bytes each; blk: the table's entry
+    auto load_tile = [&](int t, int buf, int blk) {
+      if (t < tiles && t * kSelTile + page_of_thread < last) {
+        blk = clamp_block(blk, P.num_blocks);
         const int8_t* src = P.keys + static_cast<size_t>(blk) * kD;
-        const uint32_t dst = ptx::smem_u32(s_keys) + (buf * kSelTile + (tid >> 3)) * kSelStride;
+        const uint32_t dst = ptx::smem_u32(s_keys) + (buf * kSelTile + page_of_thread) * kSelStride;
         for (int u = tid & 7; u < kD / 16; u += 8)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * u),
                        "l"(src + 16 * u)
@@ -291,20 +387,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    auto entry_of = [&](int t) {
+      const int p = t * kSelTile + page_of_thread;
+      return t < tiles && p < last ? table[p] : 0;
+    };
     for (int h0 = 0; h0 < P.h_q; h0 += kSelHeads) {
-      load_tile(rank, 0);
-      if (h0 > 0) cluster_arrive();  // the previous pass is done with the codes
+      if (h0 > 0) {
+        entry = entry_of(rank);
+        if (h0 + row0 < P.h_q && row0 < kSelHeads) load_row(h0 + row0, raw);
+        cluster_arrive();  // the previous pass is done with the codes
+      }
+      load_tile(rank, 0, entry);
+      entry = entry_of(rank + nrank);
       bool stored = false;
       const int nh = min(kSelHeads, P.h_q - h0);
-      for (int r = rank + nrank * warp; r < nh; r += nrank * (kSelThreads / 32)) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            P.q + (static_cast<size_t>(pair) * P.h_q + h0 + r) * kD);
-        uint4 w[3];
-#pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          const int u = lane + 32 * j;
-          w[j] = u < kD / 8 ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-        }
+      for (int r = row0; r < nh; r += row_step) {
+        const uint4 w[3] = {raw[0], raw[1], raw[2]};
+        if (r + row_step < nh) load_row(h0 + r + row_step, raw);
         float x[3][8];
         float amax = 0.f;
 #pragma unroll
@@ -320,11 +419,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const float scale = int8_scale(amax);
-        const bool plain = !(scale > 0x1p-100f && scale < 0x1p+100f);
-        const float inv = plain ? 0.f : 1.f / scale;
         uint2 code[3];
+        if (scale > 0x1p-100f && scale < 0x1p+100f) {
+          const float inv = __frcp_rn(scale);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) code[j] = int8_codes8(x[j], scale, inv, plain);
+          for (int j = 0; j < 3; ++j) code[j] = int8_codes8(x[j], scale, inv);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 3; ++j)
+            code[j] = int8_codes8_by_division(make_float4(x[j][0], x[j][1], x[j][2], x[j][3]),
+                                              make_float4(x[j][4], x[j][5], x[j][6], x[j][7]),
+                                              scale);
+        }
         if (!stored) {
           __syncwarp();
           cluster_wait();
@@ -343,69 +449,85 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
       cluster_arrive();  // this warp's codes are stored
       cluster_wait();
 
-      const int hq4 = warp >> 2;  // heads 32 hq4 .. + 31
-      const int pg = warp & 3;    // pages 16 pg .. + 15 of the tile
+      // 16 heads a warp, and 16 pages of a tile, or 32 where more than 64 heads
+      // leave only two warps to 16 heads
+      const bool wide = nh > 64;
+      const int hg = wide ? warp >> 1 : warp >> 2;
+      const int page0 = wide ? 32 * (warp & 1) : 16 * (warp & 3);
+      const bool active = 16 * hg < nh;
       const bool final_pass = h0 + kSelHeads >= P.h_q;
+      // the table's entry of the page whose score this thread finishes next
+      int scale_entry = 0;
+      if (tid < kSelTile && rank * kSelTile + tid < last) scale_entry = table[rank * kSelTile + tid];
+      uint32_t a[kD / 32][4];  // A tiles: 16 heads x 32 bytes
+      float unit[2] = {0.f, 0.f};
+      if (active) {
+        const uint32_t a0 = ptx::smem_u32(s_q) + (16 * hg + (lane & 15)) * kSelStride +
+                            16 * (lane >> 4);
+#pragma unroll
+        for (int k = 0; k < kD / 32; ++k) ldmatrix_x4(a[k], a0 + 32 * k);
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) unit[hi] = s_qscale[16 * hg + 8 * hi + (lane >> 2)];
+      }
       for (int t = rank, i = 0; t < tiles; t += nrank, ++i) {
-        load_tile(t + nrank, (i + 1) & 1);
+        load_tile(t + nrank, (i + 1) & 1, entry);
+        entry = entry_of(t + 2 * nrank);
         const int p = t * kSelTile + tid;
         float key_scale = 0.f, prev = -INFINITY;
         if (tid < kSelTile && p < last) {
-          key_scale = P.scales[clamp_block(table[p], P.num_blocks)];
+          key_scale = P.scales[clamp_block(scale_entry, P.num_blocks)];
           if (h0 > 0) prev = __uint_as_float(scores[p]);
         }
+        const int pn = p + nrank * kSelTile;
+        if (tid < kSelTile && pn < last) scale_entry = table[pn];
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();  // the tile's keys are in shared memory
-        if (32 * hq4 < nh) {
-          int acc[2][2][4];
+        if (active) {
+          int acc[4][4];  // 16 heads x 8 pages each
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[m][n][e] = 0;
-          // ldmatrix rows: A tiles (16 heads x 32 bytes) and a B tile (16 pages x 32 bytes)
-          const uint32_t a0 = ptx::smem_u32(s_q) + (32 * hq4 + (lane & 15)) * kSelStride +
-                              16 * (lane >> 4);
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0;
+          // B tiles (16 pages x 32 bytes)
           const uint32_t b0 = ptx::smem_u32(s_keys) +
-                              ((i & 1) * kSelTile + 16 * pg + (lane & 7) + 8 * (lane >> 4)) *
+                              ((i & 1) * kSelTile + page0 + (lane & 7) + 8 * (lane >> 4)) *
                                   kSelStride +
                               16 * ((lane >> 3) & 1);
-#pragma unroll 6
+#pragma unroll
           for (int k = 0; k < kD / 32; ++k) {
-            uint32_t a[2][4], bq[4];
-            ldmatrix_x4(bq, b0 + 32 * k);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) ldmatrix_x4(a[m], a0 + 16 * m * kSelStride + 32 * k);
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int n = 0; n < 2; ++n) mma_s8(acc[m][n], a[m], bq[2 * n], bq[2 * n + 1]);
+            uint32_t b[4];
+            ldmatrix_x4(b, b0 + 32 * k);
+            mma_s8(acc[0], a[k], b[0], b[1]);
+            mma_s8(acc[1], a[k], b[2], b[3]);
+            if (wide) {
+              ldmatrix_x4(b, b0 + 16 * kSelStride + 32 * k);
+              mma_s8(acc[2], a[k], b[0], b[1]);
+              mma_s8(acc[3], a[k], b[2], b[3]);
+            }
           }
-          // max over the warp's 32 heads of s_h * dot, per page
+          // max over the 16 heads of s_h * dot, per page
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 4; ++n) {
+            if (n >= 2 && !wide) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float v = -INFINITY;
 #pragma unroll
-              for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int hi = 0; hi < 2; ++hi) {
-                  const int r = 32 * hq4 + 16 * m + 8 * hi + (lane >> 2);
-                  if (r < nh) v = fmaxf(v, static_cast<float>(acc[m][n][2 * hi + e]) * s_qscale[r]);
-                }
+              for (int hi = 0; hi < 2; ++hi)
+                if (16 * hg + 8 * hi + (lane >> 2) < nh)
+                  v = fmaxf(v, static_cast<float>(acc[n][2 * hi + e]) * unit[hi]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-              if (lane < 4) s_best[hq4][16 * pg + 8 * n + 2 * lane + e] = v;
+              if (lane < 4) s_best[hg][page0 + 8 * n + 2 * lane + e] = v;
             }
+          }
         }
         __syncthreads();  // s_best is complete, the tile's buffer free
         if (tid < kSelTile && p < last) {
           float v = prev;
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (32 * g < nh) v = fmaxf(v, s_best[g][tid]);
+          for (int g = 0; g < kSelHeads / 16; ++g)
+            if (16 * g < nh) v = fmaxf(v, s_best[g][tid]);
           // + 0: a product that underflows to -0 ties with 0
           scores[p] = final_pass ? max(order_key(v * key_scale + 0.f), 1u) : __float_as_uint(v);
         }
@@ -421,8 +543,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
     ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x73);
   int32_t* out_table = P.taken_table + static_cast<size_t>(pair) * P.width;
   int32_t* out_pages = P.pages ? P.pages + static_cast<size_t>(pair) * P.topk : nullptr;
-  auto take = [&](int at, int page) {
-    out_table[at] = clamp_block(table[page], P.num_blocks);
+  auto take = [&](int at, int page, int entry_of_page) {
+    out_table[at] = clamp_block(entry_of_page, P.num_blocks);
     if (out_pages) out_pages[at] = page;
   };
   const int count = min(last + 1, P.topk);  // pages taken
@@ -430,56 +552,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
   if (out_pages)
     for (int p = count + tid; p < P.topk; p += kSelThreads) out_pages[p] = -1;
   if (last < P.topk) {
-    for (int p = tid; p <= last; p += kSelThreads) take(p, p);
+    for (int p = tid; p <= last; p += kSelThreads) take(p, p, table[p]);
     return;
   }
-  if (tid == 0) take(P.topk - 1, last);
+  if (tid == 0) take(P.topk - 1, last, table[last]);
   if (!choose) return;
   int need = P.topk - 1;  // pages to take before the last one
-  if (last <= kSelThreads * kSelPerThread) {
-    // thread t keeps the keys of pages n t .. n t + n - 1; border: the highest T
-    // with at least `need` keys >= T, found from its top bit down, or the first
-    // T on the way with exactly `need`
-    const int n = (last + kSelThreads - 1) / kSelThreads;
-    uint32_t key[kSelPerThread];
-#pragma unroll
-    for (int k = 0; k < kSelPerThread; ++k)
-      key[k] = k < n && n * tid + k < last ? __ldcg(scores + n * tid + k) : 0u;  // 0: no page
-    uint32_t border = 0;
-    int at_least = -1;  // keys >= border
-    for (int bit = 31; bit >= 0 && at_least != need; --bit) {
-      const uint32_t probe = border | (1u << bit);
-      int c = 0;
-#pragma unroll
-      for (int k = 0; k < kSelPerThread; ++k) c += key[k] >= probe;
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0) s_count[bit & 1][warp] = c;
-      __syncthreads();  // the other half of s_count is written next
-      c = __reduce_add_sync(0xffffffffu, lane < kSelThreads / 32 ? s_count[bit & 1][lane] : 0);
-      if (c >= need) {
-        border = probe;
-        at_least = c;
-      }
-    }
-    int above = 0, equal = 0;
-#pragma unroll
-    for (int k = 0; k < kSelPerThread; ++k) {
-      above += key[k] > border;
-      equal += key[k] == border;
-    }
-    int total;
-    const int before = block_exclusive_scan<kSelThreads>(above | (equal << 16), &total);
-    need -= total & 0xFFFF;  // of the keys equal to the border
-    int g = before & 0xFFFF, q = before >> 16;
-#pragma unroll
-    for (int k = 0; k < kSelPerThread; ++k) {
-      const bool eq = key[k] == border;
-      if (key[k] > border || (eq && q < need)) take(g + min(q, need), n * tid + k);
-      g += key[k] > border;
-      q += eq;
-    }
-    return;
-  }
+  // two keys a thread up to 1024 pages (65536 tokens), eight up to 4096
+  if (last <= 2 * kSelThreads)
+    return select_block<2>(scores, table, last, need, take);
+  if (last <= kSelPerThread * kSelThreads)
+    return select_block<kSelPerThread>(scores, table, last, need, take);
   // more pages than the registers hold: radix selection of the border, four
   // passes of eight bits over the score array, then chunks in page order
   uint32_t prefix = 0;
@@ -512,7 +595,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
     int total;
     const int before = block_exclusive_scan<kSelThreads>(gt | (eq << 16), &total);
     const int g = gt0 + (before & 0xFFFF), q = eq0 + (before >> 16);
-    if (gt || (eq && q < need)) take(g + min(q, need), base + tid);
+    if (gt || (eq && q < need)) take(g + min(q, need), base + tid, table[base + tid]);
     gt0 += total & 0xFFFF;
     eq0 += total >> 16;
   }

@@ -289,6 +289,32 @@ def test_negative_scores_are_ordered():
     c.check(c.run(4), 4)
 
 
+@pytest.mark.parametrize("kind", ["halves", "random", "tiny", "huge"])
+def test_query_codes(kind):
+    """One head against one-hot keys: the score of page p is the code of dim p, so the order of
+    the pages shows the codes."""
+    c = Case([64 * 577], h_q=1, seed=21, spare=0)
+    c.keys[c.table[0, :576].long()] = torch.diag(torch.full((576,), 127)).to(torch.int8)
+    c.scales[:] = 1.0
+    g = torch.Generator().manual_seed(22)
+    if kind == "halves":  # scale 1: whole numbers and halves, where ties go to the even code
+        x = torch.arange(576) / 2.0 - 100
+        x[0] = 127.0
+        x = x.clamp(-127, 127)
+    else:
+        x = torch.randn(576, generator=g)
+        # below and above the range where the reciprocal of the scale is used
+        x = x * {"random": 1.0, "tiny": 2.0 ** -105, "huge": 2.0 ** 110}[kind]
+    c.q[0, 0, 0] = x.to(torch.bfloat16)
+    c.cache[:] = 0
+    q = c.q.cuda()
+    for topk in (2, 17, 100, 288, 400, 575):
+        pages = B.mla_page_sparse_decode(q, c.cache.cuda(), c.keys.cuda(), c.scales.cuda(),
+                                         c.table.cuda(), c.sl(), topk)[2]
+        assert pages[0, 0].tolist() == c.select(0, 0, topk)
+    assert B.device_status() == 0
+
+
 def test_all_pages_taken_is_the_dense_decode():
     c = Case([700, 90, 0], h_q=32, s_q=2, seed=12)
     out, lse, _ = c.run(c.table.shape[1])
