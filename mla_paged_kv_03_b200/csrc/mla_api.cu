@@ -590,7 +590,7 @@ int shared_units(int batch, int rows_per_kv, int prefix_len, SharedUnits* su) {
                 "at most %d row groups of 128 (got %lld over the prefix, %lld over own tokens)",
                 mla::kPlanMaxBatch, n_prefix, batch * groups);
   const long long cost =
-      n_prefix * (mla::kPlanOverheadPair +
+      n_prefix * (mla::kPlanOverheadShared +
                   2LL * mla::kPlanTileCost * mla::granules_of(prefix_len, 2));
   MLA_CHECK_ARG(cost <= mla::kPlanMaxTotal / 2, "rows * prefix_len too large for the planner");
   su->n_prefix = static_cast<int>(n_prefix);
@@ -1169,7 +1169,7 @@ int mla_shared_prefix_get_metadata(const int32_t* cache_seqlens, int batch, int 
                 "int32 arrays must be 4-byte aligned");
   mla::mla_shared_plan_kernel<<<1, mla::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       cache_seqlens, su.units, su.n_prefix, prefix_len, su.own_groups, num_sm_parts,
-      mla::plan_params(128), metadata, num_splits);
+      mla::plan_params_shared(rows_per_kv), metadata, num_splits);
   MLA_CUDA(cudaGetLastError());
   return MLA_OK;
 }

@@ -68,6 +68,16 @@ MLA_HD inline PlanParams plan_params(int heads_per_kv) {
   return {kPlanOverheadPair, 2, 0};
 }
 
+// Of a shared-prefix decode with `rows_per_kv` query rows per sequence.  What a
+// unit over a sequence's own tokens costs beside its tiles is mostly the stores
+// of its rows' partials.  B200, step us for overheads of 8 and 16: 128 rows, 64
+// sequences behind 16384 tokens 279 and 248; 64 rows, 100 behind 8000 136 and
+// 119; 32 rows, 128 behind 8000 87 and 91; 8 rows, 200 behind 8000 66 and 75.
+constexpr int kPlanOverheadShared = 16, kPlanOverheadSharedFewRows = 8;
+MLA_HD inline PlanParams plan_params_shared(int rows_per_kv) {
+  return {rows_per_kv > 32 ? kPlanOverheadShared : kPlanOverheadSharedFewRows, 2, 0};
+}
+
 // Metadata row per SM part: {begin_b, begin_tile, end_b, end_tile,
 // first_split, 0, 0, 0}; end_tile is exclusive within batch end_b (it may pass
 // that sequence's last tile, see the planner below).
