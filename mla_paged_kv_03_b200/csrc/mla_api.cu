@@ -1294,12 +1294,18 @@ int mla_page_keys_update(const void* kcache, int num_blocks, const int32_t* bloc
   p.block_table = block_table;
   p.max_pages = max_pages;
   p.seqlens = cache_seqlens;
+  p.batch = batch;
   p.tail = tail_pages < max_pages ? tail_pages : max_pages;
   p.keys = page_keys;
   p.scales = page_scales;
+  MLA_CUDA(allow_smem<mla::mla_page_keys_kernel>(mla::kKeySmem));
+  int dev = 0, sms = 0;
+  MLA_CUDA(cudaGetDevice(&dev));
+  MLA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  const long long items = static_cast<long long>(p.tail) * batch;
   // an ordinary launch: earlier work of the stream may be writing the cache
-  mla::mla_page_keys_kernel<<<dim3(p.tail, batch), mla::kKeyThreads, 0,
-                              static_cast<cudaStream_t>(stream)>>>(p);
+  mla::mla_page_keys_kernel<<<static_cast<unsigned>(items < sms ? items : sms), mla::kKeyThreads,
+                              mla::kKeySmem, static_cast<cudaStream_t>(stream)>>>(p);
   MLA_CUDA(cudaGetLastError());
   return MLA_OK;
 }

@@ -42,78 +42,176 @@ struct PageKeysParams {
   const int32_t* block_table;
   int max_pages;
   const int32_t* seqlens;
+  int batch;
   int tail;          // the last `tail` pages of each sequence
   int8_t* keys;      // [num_blocks, 576]
   float* scales;     // [num_blocks]
 };
 
 constexpr int kKeyUnits = kD / 8;      // 16-byte units of a row
-constexpr int kKeyRowGroups = 4;       // threads that share a unit, each every 4th row
-constexpr int kKeyThreads = kKeyUnits * kKeyRowGroups;  // 288
+constexpr int kKeyRowGroups = 8;       // threads that share a unit, each every 8th row
+constexpr int kKeySummers = kKeyUnits * kKeyRowGroups;  // 576 threads: also one per dim
+constexpr int kKeyThreads = kKeySummers + 32;           // and a warp that fetches
+constexpr int kKeyHalf = kPage / 2;    // rows of a stage
+constexpr int kKeyStages = 4;
+constexpr int kKeyStageBytes = kKeyHalf * kD * 2;  // 36864
+// Partial sums: [row group][pair of a unit's dims][unit] two doubles, a pair's
+// units padded so that neither the stores (a thread per unit) nor the loads (a
+// thread per dim) meet in a bank more than twice.
+constexpr int kKeyPairStride = kKeyUnits + 4;
+constexpr int kKeySmem = kKeyStages * kKeyStageBytes + kKeyRowGroups * 4 * kKeyPairStride * 16;
 
-// grid (tail, batch), one CTA per page.  The sums are formed in fp64, where 64
-// bf16 values add exactly unless they lie 39 binades apart: the code does not
-// depend on the order, and a mean next to a rounding border is decided by its
-// value.  HBM bound: 73.7 kB read a page.
-__global__ void __launch_bounds__(kKeyThreads) mla_page_keys_kernel(const PageKeysParams P) {
-  __shared__ double s_sum[kKeyRowGroups][kD];
-  __shared__ float s_max[kKeyThreads / 32];
-  const int b = blockIdx.y;
-  int L = P.seqlens[b];
-  if (L > P.max_pages * kPage) {
-    if (threadIdx.x == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x72);
-    L = P.max_pages * kPage;
+// Untiled bulk copy of `bytes` (a multiple of 16) to this CTA's shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(ptx::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+
+// The two bf16 values of a word as the high words of doubles, 2^896 times too
+// small: exponent and fraction keep their bits, which are read in the wider
+// format's place (exact for every finite value, subnormal ones too).
+__device__ __forceinline__ double low_bf16_scaled(uint32_t w) {
+  return __hiloint2double((static_cast<int>(w << 16) >> 3) & 0x8FFFFFFF, 0);
+}
+__device__ __forceinline__ double high_bf16_scaled(uint32_t w) {
+  return __hiloint2double((static_cast<int>(w) >> 3) & 0x8FFFE000, 0);
+}
+
+// One CTA per SM goes over the (page, sequence) places tail * batch, page by
+// page.  The rows of a page that the sequence has lie in one piece, which comes
+// in by bulk copies of 32 rows into four stages, so that two pages are in
+// flight while one is summed; a warp of its own looks up the next page behind
+// the sums.  The sums are formed in fp64, where 64 bf16 values add exactly
+// unless they lie 39 binades apart: the code does not depend on the order, and
+// a mean next to a rounding border is decided by its value.  Converting bf16 to
+// fp64 at the conversion unit's rate (16 a clock per SM) costs more than the
+// page's share of HBM time; placing the bits does not.
+__global__ void __launch_bounds__(kKeyThreads, 1) mla_page_keys_kernel(const PageKeysParams P) {
+  extern __shared__ __align__(128) uint8_t s_buf[];
+  __shared__ uint64_t s_full[kKeyStages];
+  __shared__ uint32_t s_max[kKeySummers / 32];
+  __shared__ int s_blk[kKeyStages], s_rows[kKeyStages];  // of the pages in flight; 0 rows: none
+  double2* s_sum = reinterpret_cast<double2*>(s_buf + kKeyStages * kKeyStageBytes);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool fetcher = tid == kKeySummers;
+  const bool summer = tid < kKeySummers;
+  if (fetcher) {
+    for (int i = 0; i < kKeyStages; ++i) ptx::mbar_init(&s_full[i], 1);
+    ptx::fence_mbar_init();
   }
-  const int page = (L + kPage - 1) / kPage - P.tail + static_cast<int>(blockIdx.x);
-  if (L <= 0 || page < 0) return;
-  const int blk = clamp_block(P.block_table[static_cast<size_t>(b) * P.max_pages + page],
-                              P.num_blocks);
-  const int n = min(kPage, L - page * kPage);
-  const int unit = threadIdx.x % kKeyUnits, group = threadIdx.x / kKeyUnits;
-  const uint4* src = reinterpret_cast<const uint4*>(P.kcache + static_cast<size_t>(blk) * kPage * kD) +
-                     unit;
-  constexpr int kRowsPerThread = kPage / kKeyRowGroups;
-  uint4 w[kRowsPerThread];
+  __syncthreads();
+  // the fetcher's state: the next place, its block and rows
+  const long long items = static_cast<long long>(P.tail) * P.batch;
+  long long item = blockIdx.x;
+  int fetched = 0, next_rows = 0, next_blk = 0;
+  auto locate = [&]() {  // the next place that holds a page
+    next_rows = 0;
+    for (; next_rows == 0 && item < items; item += gridDim.x) {
+      const int b = static_cast<int>(item / P.tail);
+      int L = P.seqlens[b];
+      if (L > P.max_pages * kPage) {
+        ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x72);
+        L = P.max_pages * kPage;
+      }
+      const int page = (L + kPage - 1) / kPage - P.tail +
+                       static_cast<int>(item - static_cast<long long>(b) * P.tail);
+      if (L <= 0 || page < 0) continue;
+      next_rows = min(kPage, L - page * kPage);
+      next_blk = clamp_block(P.block_table[static_cast<size_t>(b) * P.max_pages + page],
+                             P.num_blocks);
+    }
+  };
+  auto fetch = [&]() {  // its copies, into the stages of page `fetched`
+    const __nv_bfloat16* src = P.kcache + static_cast<size_t>(next_blk) * kPage * kD;
+    s_blk[fetched % kKeyStages] = next_blk;
+    s_rows[fetched % kKeyStages] = next_rows;
+    if (next_rows == 0) return;
 #pragma unroll
-  for (int i = 0; i < kRowsPerThread; ++i) {
-    const int row = group + kKeyRowGroups * i;
-    w[i] = row < n ? __ldg(src + row * kKeyUnits) : make_uint4(0, 0, 0, 0);
-  }
-  double sum[8];
+    for (int h = 0; h < 2; ++h) {
+      const int st = (2 * fetched + h) % kKeyStages;
+      const int rows = min(kKeyHalf, next_rows - h * kKeyHalf);
+      if (rows > 0) {
+        ptx::mbar_arrive_expect_tx(&s_full[st], rows * kD * 2);
+        bulk_load(s_buf + st * kKeyStageBytes, src + h * kKeyHalf * kD, rows * kD * 2,
+                  &s_full[st]);
+      } else {
+        ptx::mbar_arrive(&s_full[st]);
+      }
+    }
+    ++fetched;
+  };
+  if (fetcher)
+    for (int i = 0; i < kKeyStages / 2; ++i) {
+      locate();
+      fetch();
+    }
+  __syncthreads();
+  const int unit = tid % kKeyUnits, group = tid / kKeyUnits;
+  for (int done = 0;; ++done) {
+    const int n = s_rows[done % kKeyStages], blk = s_blk[done % kKeyStages];
+    if (n == 0) return;
+    bool ok = true;
+    if (fetcher) locate();
+    if (summer) {
+      double sum[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum[e] = 0.0;
+      for (int e = 0; e < 8; ++e) sum[e] = 0.0;
 #pragma unroll
-  for (int i = 0; i < kRowsPerThread; ++i) {
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      for (int h = 0; h < 2; ++h) {
+        const int st = (2 * done + h) % kKeyStages;
+        ok = ptx::mbar_wait(&s_full[st], (done / (kKeyStages / 2)) & 1, 0x74) && ok;
+        const uint4* src = reinterpret_cast<const uint4*>(s_buf + st * kKeyStageBytes) + unit;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      sum[2 * e] += static_cast<double>(__uint_as_float(u[e] << 16));
-      sum[2 * e + 1] += static_cast<double>(__uint_as_float(u[e] & 0xFFFF0000u));
+        for (int i = 0; i < kKeyHalf / kKeyRowGroups; ++i) {
+          const int row = group + kKeyRowGroups * i;
+          if (h * kKeyHalf + row < n) {
+            const uint4 w = src[row * kKeyUnits];
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sum[2 * e] += low_bf16_scaled(u[e]);
+              sum[2 * e + 1] += high_bf16_scaled(u[e]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s_sum[(group * 4 + e) * kKeyPairStride + unit] = make_double2(sum[2 * e], sum[2 * e + 1]);
+    }
+    if (!__syncthreads_and(ok)) {  // a copy did not come: wait (bounded) for the others
+      if (fetcher)
+        for (int j = done; j < fetched; ++j)
+          for (int h = 0; h < 2; ++h)
+            ptx::mbar_wait(&s_full[(2 * j + h) % kKeyStages], (j / (kKeyStages / 2)) & 1, 0x75);
+      return;
+    }
+    if (fetcher) fetch();  // into the two stages just read
+    float mean = 0.f;
+    if (summer) {  // dim tid: of pair (tid % 8) / 2 of unit tid / 8
+      double t = 0.0;
+#pragma unroll
+      for (int g = 0; g < kKeyRowGroups; ++g)
+        t += reinterpret_cast<const double*>(
+            s_sum)[((g * 4 + ((tid & 7) >> 1)) * kKeyPairStride + (tid >> 3)) * 2 + (tid & 1)];
+      t *= 0x1p+896;
+      mean = static_cast<float>(n == kPage ? t * (1.0 / kPage) : t / n);
+      // magnitudes of floats order like their bits
+      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(mean)));
+      if (lane == 0) s_max[warp] = top;
+    }
+    __syncthreads();
+    if (summer) {
+      const float scale = int8_scale(__uint_as_float(
+          __reduce_max_sync(0xffffffffu, lane < kKeySummers / 32 ? s_max[lane] : 0u)));
+      P.keys[static_cast<size_t>(blk) * kD + tid] = static_cast<int8_t>(int8_code(mean, scale));
+      if (tid == 0) P.scales[blk] = scale;
     }
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) s_sum[group][8 * unit + e] = sum[e];
-  __syncthreads();
-  float mean[2], amax = 0.f;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int d = 2 * threadIdx.x + e;
-    const double t = (s_sum[0][d] + s_sum[1][d]) + (s_sum[2][d] + s_sum[3][d]);
-    mean[e] = static_cast<float>(t / static_cast<double>(n));
-    amax = fmaxf(amax, fabsf(mean[e]));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kKeyThreads / 32; ++i) amax = fmaxf(amax, s_max[i]);
-  const float scale = int8_scale(amax);
-  char2 code;
-  code.x = static_cast<signed char>(int8_code(mean[0], scale));
-  code.y = static_cast<signed char>(int8_code(mean[1], scale));
-  reinterpret_cast<char2*>(P.keys + static_cast<size_t>(blk) * kD)[threadIdx.x] = code;
-  if (threadIdx.x == 0) P.scales[blk] = scale;
 }
 
 // ------------------------------------------------------------------ selection
