@@ -24,10 +24,17 @@
 // and its maximum takes 4, 2 or 1 shuffles.  A warp keeps its gains in registers and
 // strides over the tokens.
 //
-// Precision: the norm's sum of squares is formed in fp64, and y in fp32 with
-// the exact products' low parts carried along (one rounding, as if y were
-// formed exactly), so that a code differs from the definition's only where y
-// lies within about 2^-24 of a rounding border.
+// Precision: the squares of the norm are exact in fp32 and summed there, sixteen
+// a lane in two chains and then over the lanes (about 2^-24 of the sum at most,
+// half of that in 1/sqrt, which is formed in fp64); sums near fp32's limits are
+// formed in fp64.  y is formed in fp32 with the exact products' low parts
+// carried along (one rounding), so that a code differs from the definition's
+// only where y lies within about 2^-24 of a rounding border.
+//
+// Bound: bulk calls by instructions (some 400 a token and warp; the quotients by
+// one multiplication and one correction each, not by division), steps of a few
+// tokens by one chain of latencies, so the slot, the position and the row are
+// read side by side.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -56,16 +63,47 @@ struct AppendParams {
 };
 
 // x * g * inv with one rounding, inv = inv_hi + inv_lo: the product x g is
-// held exactly as hi + lo (Dekker's two-product by fma), and the low parts of
-// the second product are added before the result is rounded.
+// held exactly as hi + lo, and the small products join hi * inv_hi inside the
+// last fma.
 __device__ __forceinline__ float mul3_once(float x, float g, float inv_hi, float inv_lo) {
   const float hi = x * g;
   const float lo = fmaf(x, g, -hi);
-  const float y = hi * inv_hi;
-  float e = fmaf(hi, inv_hi, -y);
-  e = fmaf(hi, inv_lo, e);
-  e = fmaf(lo, inv_hi, e);
-  return y + e;
+  return fmaf(hi, inv_hi, fmaf(lo, inv_hi, hi * inv_lo));
+}
+
+// 1/sqrt(v) for v in fp32's normal range: the fp32 value (2^-22) and one Newton
+// step in fp64 (3/8 of its error squared: below 2^-44).
+__device__ __forceinline__ double inv_root(double v) {
+  const double r = static_cast<double>(rsqrtf(static_cast<float>(v)));
+  return fma(0.5 * r, fma(-v * r, r, 1.0), r);
+}
+
+// 1/sqrt(mean square + eps) of a row whose sum of squares leaves the range of
+// fp32, from its raw 16-byte units; every lane of the warp calls it.
+__device__ __noinline__ double inv_root_by_fp64(uint4 a, uint4 b, double eps) {
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  double ss = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double lo = __uint_as_float(u[e] << 16), hi = __uint_as_float(u[e] & 0xFFFF0000u);
+    ss = fma(lo, lo, fma(hi, hi, ss));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  return 1.0 / sqrt(ss * (1.0 / kNope) + eps);
+}
+
+// y / scale for eight values.  kSmall: the scale may leave the range in which
+// its reciprocal serves.
+template <bool kSmall>
+__device__ __forceinline__ void quotients8(const float* y, float scale, float* c) {
+  const float inv = __frcp_rn(scale);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) c[k] = div_by(y[k], scale, inv);
+  if (kSmall && !(scale > 0x1p-100f && scale < 0x1p+100f)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c[k] = y[k] / scale;
+  }
 }
 
 // Eight fp32 values -> eight E2M1 codes (nearest, ties to even, saturating),
@@ -104,14 +142,16 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t pair) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// bf16(code * scale) of eight codes, each product rounded once.
+// bf16(code * scale) of eight codes, each product rounded once.  kExact: the
+// product is exact in fp32 (a code of at most four significand bits times a
+// power of two or a four-bit scale).
+template <bool kExact>
 __device__ __forceinline__ uint4 scaled_bf16x8(const float* c, float scale) {
-  uint4 o;
-  o.x = ptx::pack_bf16x2(mul_round_odd(c[0], scale), mul_round_odd(c[1], scale));
-  o.y = ptx::pack_bf16x2(mul_round_odd(c[2], scale), mul_round_odd(c[3], scale));
-  o.z = ptx::pack_bf16x2(mul_round_odd(c[4], scale), mul_round_odd(c[5], scale));
-  o.w = ptx::pack_bf16x2(mul_round_odd(c[6], scale), mul_round_odd(c[7], scale));
-  return o;
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = kExact ? c[k] * scale : mul_round_odd(c[k], scale);
+  return make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
+                    ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
 }
 
 __device__ __forceinline__ uint4 pack_bf16x8(const float* y) {
@@ -144,7 +184,8 @@ __device__ __forceinline__ void rotate_unit(float* y, int u, bool mine, float cs
 }
 
 template <int kRowBytes>
-__global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const AppendParams P) {
+__global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
+    mla_append_kernel(const AppendParams P) {
   static_assert(kRowBytes == kRow1152 || kRowBytes == kRow656 || kRowBytes == kRow528 ||
                     kRowBytes == kRow288,
                 "1152-, 656-, 528- or 288-byte rows");
@@ -153,6 +194,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const App
   constexpr int kGroupLanes = kRowBytes == kRow656 ? 16 : kRowBytes == kRow528 ? 4 : 2;
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
+  const double turns = P.turns[lane];
   float g[2][8];
 #pragma unroll
   for (int j = 0; j < 2; ++j)
@@ -162,10 +204,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const App
   for (long long t = (long long)blockIdx.x * kAppendWarps + warp; t < P.n;
        t += (long long)gridDim.x * kAppendWarps) {
     const int slot = P.slots[t];
-    if (slot < 0 || slot >= P.num_slots) {  // no slot: whatever the row holds is not read
-      if (slot >= 0 && lane == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x71);
-      continue;
-    }
+    const int position = P.positions ? P.positions[t] : 0;
     const __nv_bfloat16* src = P.kv + t * P.kv_stride;
     uint4 raw[3];
 #pragma unroll
@@ -173,10 +212,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const App
       raw[j] = *reinterpret_cast<const uint4*>(src + (lane + 32 * j) * 8);
     raw[2] = make_uint4(0, 0, 0, 0);
     if (kWide && lane < 8) raw[2] = *reinterpret_cast<const uint4*>(src + kNope + lane * 8);
+    if (slot < 0 || slot >= P.num_slots) {  // no slot: whatever the row holds is not used
+      if (slot >= 0 && lane == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x71);
+      continue;
+    }
     float cs = 1.f, sn = 0.f;
     if (P.positions) {
       // the angle in turns, its whole turns dropped in fp64, the rest in fp32
-      const double a = static_cast<double>(P.positions[t]) * P.turns[lane];
+      const double a = static_cast<double>(position) * turns;
       sincospif(2.f * static_cast<float>(a - rint(a)), &sn, &cs);
     }
     float y[2][8], yr[8];
@@ -185,15 +228,18 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const App
     unpack_bf16x8(raw[2], yr);
 
     if (P.gain) {
-      double ss = 0.0;
+      float s0 = 0.f, s1 = 0.f;  // the squares are exact in fp32
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int e = 0; e < 8; ++e) {
+        s0 = fmaf(y[0][e], y[0][e], s0);
+        s1 = fmaf(y[1][e], y[1][e], s1);
+      }
+      float s = s0 + s1;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)  // the squares are exact in fp64
-          ss = fma(static_cast<double>(y[j][e]), static_cast<double>(y[j][e]), ss);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const double inv = 1.0 / sqrt(ss * (1.0 / kNope) + P.eps);
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const double inv = s > 0x1p-80f && s < 0x1p+100f
+                             ? inv_root(static_cast<double>(s) * (1.0 / kNope) + P.eps)
+                             : inv_root_by_fp64(raw[0], raw[1], P.eps);
       const float inv_hi = static_cast<float>(inv);
       const float inv_lo = static_cast<float>(inv - static_cast<double>(inv_hi));
 #pragma unroll
@@ -244,16 +290,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const App
         } else if constexpr (kRowBytes == kRow656) {
           scale = amax > 0.f ? amax / 448.f : 1.f;
           if (!(scale > 0.f)) scale = 1.f;  // absmax/448 below the least fp32 value
-#pragma unroll
-          for (int k = 0; k < 8; ++k) c[k] = y[j][k] / scale;
+          quotients8<true>(y[j], scale, c);
           if (lane % kGroupLanes == 0)
             *reinterpret_cast<float*>(row + kNope + 4 * group) = scale;
         } else {
-          uint32_t code = cvt_e4m3x4(amax > 0.f ? amax / 6.f : 1.f, 0.f, 0.f, 0.f) & 0xFFu;
-          if (code == 0) code = 0x38;  // 1.0
+          uint32_t code = cvt_e4m3x4(div_by(amax, 6.f, 1.f / 6.f), 0.f, 0.f, 0.f) & 0xFFu;
+          if (code == 0) code = 0x38;  // 1.0, of a zero or tiny group
           scale = e4m3x2_to_float2(code).x;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) c[k] = y[j][k] / scale;
+          quotients8<false>(y[j], scale, c);
           if (lane % kGroupLanes == 0) row[kNope / 2 + group] = static_cast<uint8_t>(code);
         }
         if constexpr (kRowBytes == kRow288) {
@@ -266,7 +310,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const App
               c[2 * k] = f.x;
               c[2 * k + 1] = f.y;
             }
-            *reinterpret_cast<uint4*>(out + u * 8) = scaled_bf16x8(c, scale);
+            *reinterpret_cast<uint4*>(out + u * 8) = scaled_bf16x8<true>(c, scale);
           }
         } else {
           const uint32_t lo = cvt_e4m3x4(c[0], c[1], c[2], c[3]);
@@ -279,7 +323,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const App
               c[2 * k] = f.x;
               c[2 * k + 1] = f.y;
             }
-            *reinterpret_cast<uint4*>(out + u * 8) = scaled_bf16x8(c, scale);
+            *reinterpret_cast<uint4*>(out + u * 8) = scaled_bf16x8<kRowBytes == kRow528>(c, scale);
           }
         }
       }

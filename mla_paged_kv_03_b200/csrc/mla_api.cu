@@ -1444,9 +1444,11 @@ int mla_cache_append(const void* kv, int64_t kv_stride, int d, const int32_t* sl
   p.positions = positions;
   p.gain = norm_gain;
   p.eps = eps;
-  for (int k = 0; k < mla::kRope / 2; ++k)
-    p.turns[k] = std::pow(static_cast<double>(rope_base), -2.0 * k / mla::kRope) /
-                 6.283185307179586476925286766559;
+  // base^(-2k/64) / (2 pi): products in the host's 64-bit significands, so that
+  // the last is off by about 2^-59 and rounds to fp64 as the power itself would
+  const long double ratio = std::pow(static_cast<long double>(rope_base), -2.0L / mla::kRope);
+  long double turns = 1.0L / 6.283185307179586476925286766559L;
+  for (int k = 0; k < mla::kRope / 2; ++k, turns *= ratio) p.turns[k] = static_cast<double>(turns);
   p.n = n;
   p.cache = static_cast<uint8_t*>(kcache);
   p.num_slots = num_slots;

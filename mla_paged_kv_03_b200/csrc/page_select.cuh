@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "combine_kernel.cuh"
+#include "sparse_gather.cuh"
 
 namespace mla {
 
@@ -314,18 +315,14 @@ __device__ __noinline__ uint2 int8_codes8_by_division(float4 lo, float4 hi, floa
   return make_uint2(o[0], o[1]);
 }
 
-// int8_code of eight finite values, inv = 1/scale correctly rounded: one step
-// from q = x inv, q + (x - q scale) inv, is then the correctly rounded quotient
-// (Markstein, IBM J. Res. Dev. 34, 1990).  Adding 1.5 * 2^23 rounds it to a
-// whole number, ties to even, whose low byte is the code.
+// int8_code of eight finite values, inv = 1/scale.  Adding 1.5 * 2^23 rounds the
+// quotient to a whole number, ties to even, whose low byte is the code.
 __device__ __forceinline__ uint2 int8_codes8(const float* x, float scale, float inv) {
   constexpr float kMagic = 12582912.f;
   uint32_t m[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float q = __fmul_rn(x[e], inv);
-    m[e] = __float_as_uint(__fadd_rn(__fmaf_rn(__fmaf_rn(-q, scale, x[e]), inv, q), kMagic));
-  }
+  for (int e = 0; e < 8; ++e)
+    m[e] = __float_as_uint(__fadd_rn(div_by(x[e], scale, inv), kMagic));
   uint2 o;
   o.x = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
   o.y = __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410);

@@ -81,6 +81,15 @@ __device__ __forceinline__ float mul_round_odd(float a, float b) {
   return e != 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
 }
 
+// x / d correctly rounded, inv = 1/d correctly rounded: one step from q = x inv
+// (Markstein, IBM J. Res. Dev. 34, 1990).  For d between 2^-100 and 2^100 and
+// quotients that do not overflow; one that underflows may be off in its last
+// places.
+__device__ __forceinline__ float div_by(float x, float d, float inv) {
+  const float q = __fmul_rn(x, inv);
+  return __fmaf_rn(__fmaf_rn(-q, d, x), inv, q);
+}
+
 // Eight E2M1 codes (4 bytes, low nibble first) -> four f16x2 pairs through the
 // hardware pair conversion (byte j -> pair j, low nibble -> low half).
 __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {

@@ -68,6 +68,14 @@ def e4m3(b):
     return b.contiguous().view(torch.float8_e4m3fn).double()
 
 
+def bf16_once(x):
+    """fp64 -> the nearest bf16 (ties to even), as fp64.  torch rounds to fp32 on the way: the
+    product -224 * 0x1.2edb6ep-7 = -0x1.0900004p+1 of a code and an fp32 scale lies above the tie
+    0x1.09p+1 and goes to 0x1.0ap+1, but its fp32 rounding is the tie, which goes to 0x1.08p+1."""
+    step = torch.exp2((torch.frexp(x)[1].clamp(min=-125) - 8).double())
+    return torch.round(x / step) * step
+
+
 def check_bf16(got, y, size, what):
     err = (got.double() - y).abs()
     bound = y.abs() * 2.0 ** -8 * (1 + 2.0 ** -14) + SLACK * size
@@ -125,9 +133,8 @@ def check_rows(fmt, raw, y, size, stands=None):
         bound = torch.where(v.abs() < 2, 0.25, torch.where(v.abs() < 4, 0.5, 1.0))
         assert ((value - v).abs() <= bound + SLACK * size / scale).all()
     if stands is not None:
-        dense = (value * scale).to(torch.float64)
         # code * scale is exact in fp64: the row is its bf16 rounding
-        assert torch.equal(stands[:, :512], dense.to(torch.bfloat16))
+        assert torch.equal(stands[:, :512].double(), bf16_once(value * scale))
         if fmt == "656":
             assert torch.equal(stands[:, 512:], raw[:, 528:].contiguous().view(torch.bfloat16))
 
@@ -182,6 +189,17 @@ def test_append_sizes(fmt, n):
 @pytest.mark.parametrize("norm,rope", [(False, False), (True, False), (False, True)])
 def test_append_without_norm_or_rotation(fmt, norm, rope):
     run(fmt, 130, norm=norm, rope=rope, seed=3)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("size,eps", [(1e25, 1e-6), (3e37, 0.0), (1e-13, 0.0), (1e-28, 0.0),
+                                      (1e-37, 0.0)])
+def test_norm_of_rows_whose_squares_leave_fp32(fmt, size, eps):
+    g = torch.Generator().manual_seed(9)
+    x = (torch.rand((40, width(fmt)), generator=g) + 0.5) * size
+    # (the dims behind the norm's 512 keep an ordinary size)
+    x[:, 512:] = torch.randn((40, width(fmt) - 512), generator=g)
+    run(fmt, 40, values=x.to(torch.bfloat16), eps=eps, seed=10)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
