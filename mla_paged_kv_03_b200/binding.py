@@ -8,6 +8,7 @@ missing or was built for another GPU, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -235,7 +236,7 @@ def _workspace(nbytes, device, workspace):
     if workspace is not None:
         _require(workspace.numel() * workspace.element_size() >= nbytes, "workspace too small")
         return workspace
-    return torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=device)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 # ------------------------------------------------------------------ decode
@@ -587,12 +588,12 @@ def mla_shared_prefix_decode_fwd(q: torch.Tensor, kcache: torch.Tensor,
         raise ValueError(f"metadata and num_splits must be the plan, on cuda:{index}")
     if not q.is_contiguous():
         q = q.contiguous()
+    dev = q.device
     if out is None:
-        out = q.new_empty((b, s_q, h_q, 512))
+        out = torch.empty(b, s_q, h_q, 512, dtype=torch.bfloat16, device=dev)
     if lse is None:
-        lse = torch.empty((b, s_q, h_q), dtype=torch.float32, device=q.device)
-    ws = _workspace(mla_shared_prefix_workspace_size(b, s_q * h_q, prefix_len, num_sm_parts),
-                    q.device, workspace)
+        lse = torch.empty(b, s_q, h_q, dtype=torch.float32, device=dev)
+    ws = _workspace(_shared_prefix_bytes(b, s_q * h_q, prefix_len, num_sm_parts), dev, workspace)
     _call(index, lib().mla_shared_prefix_decode_fwd, q.data_ptr(), kcache.data_ptr(),
           kcache.shape[0], None if pt is None else pt.data_ptr(), prefix_len, bt.data_ptr(),
           bt.shape[1], sl.data_ptr(), b, s_q, h_q, kcache.shape[2], 512,
@@ -645,6 +646,13 @@ def mla_page_sparse_workspace_size(batch, s_q, h_q, d_v, max_pages, topk_pages,
     return out.value
 
 
+# Functions of whole numbers alone, asked for in every call.
+_num_sm_parts = functools.lru_cache(64)(
+    lambda heads, index: mla_num_sm_parts(heads, 1, torch.device("cuda", index)))
+_page_sparse_bytes = functools.lru_cache(256)(mla_page_sparse_workspace_size)
+_shared_prefix_bytes = functools.lru_cache(256)(mla_shared_prefix_workspace_size)
+
+
 def mla_page_sparse_decode(q: torch.Tensor, kcache: torch.Tensor, page_keys: torch.Tensor,
                            page_scales: torch.Tensor, block_table: torch.Tensor,
                            cache_seqlens: torch.Tensor, topk_pages: int, causal: bool = True,
@@ -665,14 +673,14 @@ def mla_page_sparse_decode(q: torch.Tensor, kcache: torch.Tensor, page_keys: tor
         q = q.contiguous()
     dev, max_pages = q.device, bt.shape[1]
     if num_sm_parts is None:
-        num_sm_parts = mla_num_sm_parts(h_q, 1, dev)
-    nbytes = mla_page_sparse_workspace_size(b, s_q, h_q, d_v, max_pages, topk_pages, num_sm_parts)
+        num_sm_parts = _num_sm_parts(h_q, index)
+    nbytes = _page_sparse_bytes(b, s_q, h_q, d_v, max_pages, topk_pages, num_sm_parts)
     if out is None:
-        out = q.new_empty((b, s_q, h_q, d_v))
+        out = torch.empty(b, s_q, h_q, d_v, dtype=torch.bfloat16, device=dev)
     if lse is None:
-        lse = torch.empty((b, s_q, h_q), dtype=torch.float32, device=dev)
+        lse = torch.empty(b, s_q, h_q, dtype=torch.float32, device=dev)
     if pages is None:
-        pages = bt.new_empty((b, s_q, topk_pages))
+        pages = torch.empty(b, s_q, topk_pages, dtype=torch.int32, device=dev)
     ws = _workspace(nbytes, dev, workspace)
     _call(index, lib().mla_page_sparse_decode, q.data_ptr(), kcache.data_ptr(), nb,
           page_keys.data_ptr(), page_scales.data_ptr(), bt.data_ptr(), max_pages, sl.data_ptr(),

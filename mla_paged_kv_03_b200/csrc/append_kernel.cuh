@@ -27,9 +27,9 @@
 // Precision: the squares of the norm are exact in fp32 and summed there, sixteen
 // a lane in two chains and then over the lanes (about 2^-24 of the sum at most,
 // half of that in 1/sqrt, which is formed in fp64); sums near fp32's limits are
-// formed in fp64.  y is formed in fp32 with the exact products' low parts
-// carried along (one rounding), so that a code differs from the definition's
-// only where y lies within about 2^-24 of a rounding border.
+// formed in fp64.  y has two further roundings, of g / rms and of the product: a
+// code differs from the definition's only where y lies within a few 2^-24 of a
+// rounding border.
 //
 // Bound: bulk calls by instructions (some 400 a token and warp; the quotients by
 // one multiplication and one correction each, not by division), steps of a few
@@ -61,15 +61,6 @@ struct AppendParams {
   long long num_slots;
   __nv_bfloat16* rows;  // [n, d], or null
 };
-
-// x * g * inv with one rounding, inv = inv_hi + inv_lo: the product x g is
-// held exactly as hi + lo, and the small products join hi * inv_hi inside the
-// last fma.
-__device__ __forceinline__ float mul3_once(float x, float g, float inv_hi, float inv_lo) {
-  const float hi = x * g;
-  const float lo = fmaf(x, g, -hi);
-  return fmaf(hi, inv_hi, fmaf(lo, inv_hi, hi * inv_lo));
-}
 
 // 1/sqrt(v) for v in fp32's normal range: the fp32 value (2^-22) and one Newton
 // step in fp64 (3/8 of its error squared: below 2^-44).
@@ -107,32 +98,23 @@ __device__ __forceinline__ void quotients8(const float* y, float scale, float* c
 }
 
 // Eight fp32 values -> eight E2M1 codes (nearest, ties to even, saturating),
-// code 2i in the low nibble of byte i.
-__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v) {
+// code 2i in the low nibble of byte i, and the values that the codes stand for
+// as f16 pairs (exact), taken from the bytes before they are packed.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v, uint32_t (&h)[4]) {
   uint32_t w;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %8, %7;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %10, %9;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %12, %11;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %4, b3;\n\t"
       "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-      : "=r"(w)
+      : "=r"(w), "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return w;
-}
-
-// E2M1 code pair (low nibble first) -> two fp32 values (exact).  The byte is
-// cut out of the packed word by a shift and handed over in a 16-bit register:
-// unpacking a word that the same thread packed with mov.b32 {b0, b1, b2, b3}
-// (e2m1x8_to_f16x2 right behind cvt_e2m1x8) gave zeros for its upper two bytes.
-__device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t byte) {
-  uint32_t h;
-  asm("{\n\t.reg .b8 b0, b1;\n\t"
-      "mov.b16 {b0, b1}, %1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
-      : "=r"(h)
-      : "h"(static_cast<uint16_t>(byte)));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // E4M3 code pair -> two fp32 values (exact).
@@ -240,12 +222,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
       const double inv = s > 0x1p-80f && s < 0x1p+100f
                              ? inv_root(static_cast<double>(s) * (1.0 / kNope) + P.eps)
                              : inv_root_by_fp64(raw[0], raw[1], P.eps);
-      const float inv_hi = static_cast<float>(inv);
-      const float inv_lo = static_cast<float>(inv - static_cast<double>(inv_hi));
+      const float inv32 = static_cast<float>(inv);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[j][e] = mul3_once(y[j][e], g[j][e], inv_hi, inv_lo);
+        for (int e = 0; e < 8; ++e) y[j][e] *= g[j][e] * inv32;
     }
     if (P.positions) {
       if (kWide)
@@ -301,12 +282,13 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
           if (lane % kGroupLanes == 0) row[kNope / 2 + group] = static_cast<uint8_t>(code);
         }
         if constexpr (kRowBytes == kRow288) {
-          const uint32_t w = cvt_e2m1x8(c);
+          uint32_t h[4];
+          const uint32_t w = cvt_e2m1x8(c, h);
           *reinterpret_cast<uint32_t*>(row + u * 4) = w;
           if (out) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 f = e2m1x2_to_float2((w >> (8 * k)) & 0xFFu);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
               c[2 * k] = f.x;
               c[2 * k + 1] = f.y;
             }
