@@ -1,6 +1,7 @@
 """ctypes binding of libmla_b200 (the C ABI in include/mla.h).
 
-Argument marshalling only: every step of the decode path runs in the
+Argument marshalling only (that of the cache-side calls, which are short, in
+the extension module _torch_calls): every step of the decode path runs in the
 library's CUDA kernels.  torch supplies device memory (outputs, workspace) and
 the current CUDA stream.  There is no fallback: if the shared library is
 missing or was built for another GPU, calls raise.
@@ -8,7 +9,6 @@ missing or was built for another GPU, calls raise.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 from typing import Optional
@@ -115,6 +115,22 @@ def lib():
     return _lib
 
 
+_calls = None
+
+
+def calls():
+    """The extension module of the cache-side calls (raises if it is not built)."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _torch_calls
+        except ImportError as e:
+            raise ImportError(f"{e}: build it with `python -m mla_paged_kv_03_b200.build`") from e
+        _calls = _torch_calls
+    return _calls
+
+
 def _check(rc):
     if rc != MLA_OK:
         raise MLAError(rc, lib().mla_last_error().decode())
@@ -126,17 +142,6 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
-def _call(index, fn, *args):
-    """fn(*args, stream) with device `index` current, on its current stream."""
-    if index == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if rc != MLA_OK:
-        _check(rc)
 
 
 def _require(cond, msg):
@@ -493,39 +498,6 @@ def mla_sparse_prefill_fwd(q, kv, indices, softmax_scale=None, d_v=512, topk_len
     return out, lse
 
 
-SOFTMAX_SCALE = 1.0 / math.sqrt(D_QK)
-
-
-def _int32(t, name, shape, index):
-    """`t` as a contiguous int32 tensor of `shape` on device `index`."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}")
-    if t.dtype != torch.int32:
-        if t.dtype != torch.int64:
-            raise ValueError(f"{name} must be int32 (or int64)")
-        t = t.to(torch.int32)
-    return t if t.is_contiguous() else t.contiguous()
-
-
-def _query(q):
-    """(device index, shape) of a CUDA bf16 [b, s_q, h_q, 576] query."""
-    shape = q.shape
-    if len(shape) != 4 or shape[3] != D_QK or q.dtype != torch.bfloat16 or not q.is_cuda:
-        raise ValueError("q must be CUDA bf16 [b, s_q, h_q, 576]")
-    return q.get_device(), shape
-
-
-def _bf16_cache(kcache, index):
-    shape = kcache.shape
-    if len(shape) != 4 or shape[1] != 64 or shape[3] != D_QK or \
-            kcache.dtype != torch.bfloat16 or not kcache.is_contiguous() or index < 0 or \
-            kcache.get_device() != index:
-        raise ValueError("kcache must be contiguous CUDA bf16 [NB, 64, h_kv, 576] on the "
-                         "queries' device")
-
-
 # ------------------------------------------------------------------ shared prefix
 
 def mla_shared_prefix_workspace_size(batch, rows_per_kv, prefix_len, num_sm_parts) -> int:
@@ -552,9 +524,10 @@ def mla_shared_prefix_get_metadata(cache_seqlens: torch.Tensor, prefix_len: int,
                                                  ctypes.byref(n)))
     meta = torch.empty((num_sm_parts, 8), dtype=torch.int32, device=sl.device)
     splits = torch.empty((n.value // 4,), dtype=torch.int32, device=sl.device)
-    _call(sl.get_device(), lib().mla_shared_prefix_get_metadata, sl.data_ptr(), sl.numel(),
-          int(rows_per_kv), int(h_kv), int(prefix_len), int(num_sm_parts), meta.data_ptr(),
-          splits.data_ptr())
+    with torch.cuda.device(sl.device):
+        _check(lib().mla_shared_prefix_get_metadata(_ptr(sl), sl.numel(), int(rows_per_kv),
+                                                    int(h_kv), int(prefix_len), int(num_sm_parts),
+                                                    _ptr(meta), _ptr(splits), _stream(sl.device)))
     return meta, splits, num_sm_parts
 
 
@@ -570,56 +543,12 @@ def mla_shared_prefix_decode_fwd(q: torch.Tensor, kcache: torch.Tensor,
     blocks of the prefix; block_table [b, max_pages] and cache_seqlens [b] int32
     the sequences' own tokens behind it.  Returns (out [b, s_q, h_q, 512] bf16,
     lse [b, s_q, h_q] fp32)."""
-    index, (b, s_q, h_q, _) = _query(q)
-    _bf16_cache(kcache, index)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [b, max_pages]")
-    bt = _int32(block_table, "block_table", (b, block_table.shape[1]), index)
-    sl = _int32(cache_seqlens, "cache_seqlens", (b,), index)
-    pt = None
-    if prefix_len > 0:
-        if prefix_table is None or prefix_table.dim() != 1 or \
-                prefix_table.numel() < -(-prefix_len // 64):
-            raise ValueError("prefix_table must be [>= ceil(prefix_len / 64)]")
-        pt = _int32(prefix_table, "prefix_table", prefix_table.shape, index)
-    if metadata.numel() < 8 * num_sm_parts or metadata.dtype != torch.int32 or \
-            num_splits.dtype != torch.int32 or metadata.get_device() != index or \
-            num_splits.get_device() != index:
-        raise ValueError(f"metadata and num_splits must be the plan, on cuda:{index}")
-    if not q.is_contiguous():
-        q = q.contiguous()
-    dev = q.device
-    if out is None:
-        out = torch.empty(b, s_q, h_q, 512, dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.empty(b, s_q, h_q, dtype=torch.float32, device=dev)
-    ws = _workspace(_shared_prefix_bytes(b, s_q * h_q, prefix_len, num_sm_parts), dev, workspace)
-    _call(index, lib().mla_shared_prefix_decode_fwd, q.data_ptr(), kcache.data_ptr(),
-          kcache.shape[0], None if pt is None else pt.data_ptr(), prefix_len, bt.data_ptr(),
-          bt.shape[1], sl.data_ptr(), b, s_q, h_q, kcache.shape[2], 512,
-          SOFTMAX_SCALE if softmax_scale is None else softmax_scale, int(causal),
-          metadata.data_ptr(), num_splits.data_ptr(), num_sm_parts, ws.data_ptr(),
-          ws.numel() * ws.element_size(), out.data_ptr(), lse.data_ptr())
-    return out, lse
+    return (_calls or calls()).shared_prefix_decode(
+        q, kcache, prefix_table, prefix_len, block_table, cache_seqlens, metadata, num_splits,
+        num_sm_parts, causal, softmax_scale, out, lse, workspace)
 
 
 # ------------------------------------------------------------------ page selection
-
-def _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, index):
-    """(blocks, block_table, cache_seqlens) once the arguments are checked."""
-    _bf16_cache(kcache, index)
-    nb = kcache.shape[0]
-    if page_keys.shape != (nb, D_QK) or page_keys.dtype != torch.int8 or \
-            not page_keys.is_contiguous() or page_keys.get_device() != index:
-        raise ValueError(f"page_keys must be contiguous int8 [{nb}, 576] on cuda:{index}")
-    if page_scales.shape != (nb,) or page_scales.dtype != torch.float32 or \
-            not page_scales.is_contiguous() or page_scales.get_device() != index:
-        raise ValueError(f"page_scales must be contiguous fp32 [{nb}] on cuda:{index}")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [b, max_pages]")
-    bt = _int32(block_table, "block_table", block_table.shape, index)
-    return nb, bt, _int32(cache_seqlens, "cache_seqlens", (bt.shape[0],), index)
-
 
 def mla_page_keys_update(kcache: torch.Tensor, block_table: torch.Tensor,
                          cache_seqlens: torch.Tensor, page_keys: torch.Tensor,
@@ -627,14 +556,8 @@ def mla_page_keys_update(kcache: torch.Tensor, block_table: torch.Tensor,
     """Recompute the int8 page keys (the quantised mean of each page's rows) of
     the last `tail_pages` pages of every sequence (default: all pages).
     page_keys [NB, 576] int8 and page_scales [NB] fp32 are written in place."""
-    index = kcache.get_device()
-    nb, bt, sl = _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, index)
-    if kcache.shape[2] != 1:
-        raise ValueError("kcache must be [NB, 64, 1, 576]")
-    b, max_pages = bt.shape
-    _call(index, lib().mla_page_keys_update, kcache.data_ptr(), nb, bt.data_ptr(), max_pages,
-          sl.data_ptr(), b, max_pages if tail_pages is None else tail_pages,
-          page_keys.data_ptr(), page_scales.data_ptr())
+    (_calls or calls()).page_keys_update(kcache, block_table, cache_seqlens, page_keys,
+                                         page_scales, tail_pages)
 
 
 def mla_page_sparse_workspace_size(batch, s_q, h_q, d_v, max_pages, topk_pages,
@@ -644,13 +567,6 @@ def mla_page_sparse_workspace_size(batch, s_q, h_q, d_v, max_pages, topk_pages,
                                                 int(max_pages), int(topk_pages),
                                                 int(num_sm_parts), ctypes.byref(out)))
     return out.value
-
-
-# Functions of whole numbers alone, asked for in every call.
-_num_sm_parts = functools.lru_cache(64)(
-    lambda heads, index: mla_num_sm_parts(heads, 1, torch.device("cuda", index)))
-_page_sparse_bytes = functools.lru_cache(256)(mla_page_sparse_workspace_size)
-_shared_prefix_bytes = functools.lru_cache(256)(mla_shared_prefix_workspace_size)
 
 
 def mla_page_sparse_decode(q: torch.Tensor, kcache: torch.Tensor, page_keys: torch.Tensor,
@@ -665,30 +581,9 @@ def mla_page_sparse_decode(q: torch.Tensor, kcache: torch.Tensor, page_keys: tor
     mla_decode_fwd.  Returns (out [b, s_q, h_q, d_v] bf16, lse [b, s_q, h_q]
     fp32, pages [b, s_q, topk_pages] int32: the pages taken, ascending, -1
     behind them)."""
-    index, (b, s_q, h_q, _) = _query(q)
-    nb, bt, sl = _page_args(kcache, page_keys, page_scales, block_table, cache_seqlens, index)
-    if bt.shape[0] != b:
-        raise ValueError(f"block_table must be [{b}, max_pages]")
-    if not q.is_contiguous():
-        q = q.contiguous()
-    dev, max_pages = q.device, bt.shape[1]
-    if num_sm_parts is None:
-        num_sm_parts = _num_sm_parts(h_q, index)
-    nbytes = _page_sparse_bytes(b, s_q, h_q, d_v, max_pages, topk_pages, num_sm_parts)
-    if out is None:
-        out = torch.empty(b, s_q, h_q, d_v, dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.empty(b, s_q, h_q, dtype=torch.float32, device=dev)
-    if pages is None:
-        pages = torch.empty(b, s_q, topk_pages, dtype=torch.int32, device=dev)
-    ws = _workspace(nbytes, dev, workspace)
-    _call(index, lib().mla_page_sparse_decode, q.data_ptr(), kcache.data_ptr(), nb,
-          page_keys.data_ptr(), page_scales.data_ptr(), bt.data_ptr(), max_pages, sl.data_ptr(),
-          b, s_q, h_q, kcache.shape[2], d_v, topk_pages,
-          SOFTMAX_SCALE if softmax_scale is None else softmax_scale, int(causal), num_sm_parts,
-          ws.data_ptr(), ws.numel() * ws.element_size(), pages.data_ptr(), out.data_ptr(),
-          lse.data_ptr())
-    return out, lse, pages
+    return (_calls or calls()).page_sparse_decode(
+        q, kcache, page_keys, page_scales, block_table, cache_seqlens, topk_pages, causal,
+        softmax_scale, d_v, num_sm_parts, pages, out, lse, workspace)
 
 
 # ------------------------------------------------------------------ cache writers
@@ -704,40 +599,5 @@ def mla_cache_append(kv: torch.Tensor, slots: torch.Tensor, kcache: torch.Tensor
     strided.  slots [n] int32 physical slots (negative = padding, skipped; the
     others must differ).  `rows` (bf16, kv's shape, contiguous) receives the
     rows as the cache stands for them.  Writes into `kcache`; returns `rows`."""
-    width = kcache.shape[-1]
-    if kcache.dtype == torch.bfloat16 and width == D_QK:
-        row_bytes = 2 * D_QK
-    elif kcache.dtype == torch.uint8 and width in (656, 528, 288):
-        row_bytes = width
-    else:
-        raise ValueError("kcache must be bf16 [..., 576] or uint8 [..., 656], [..., 528] or "
-                         "[..., 288]")
-    d = D_QK if row_bytes >= 656 else 512
-    shape = kv.shape
-    if len(shape) != 2 or shape[1] != d or kv.dtype != torch.bfloat16 or not kv.is_cuda:
-        raise ValueError(f"kv must be CUDA bf16 [n, {d}] for {row_bytes}-byte cache rows")
-    index, n = kv.get_device(), shape[0]
-    if not kcache.is_contiguous() or kcache.get_device() != index:
-        raise ValueError(f"kcache must be contiguous and on cuda:{index}")
-    if n == 0:
-        return rows
-    stride, inner = kv.stride()
-    if inner != 1 or stride % 8 or (n > 1 and stride < d) or kv.data_ptr() % 16:
-        kv, stride = kv.clone(memory_format=torch.contiguous_format), d
-    slots = _int32(slots, "slots", (n,), index)
-    if positions is not None:
-        positions = _int32(positions, "positions", (n,), index)
-    if norm_gain is not None:
-        if norm_gain.shape != (512,) or norm_gain.get_device() != index:
-            raise ValueError(f"norm_gain must be [512] on cuda:{index}")
-        if norm_gain.dtype != torch.float32 or not norm_gain.is_contiguous():
-            norm_gain = norm_gain.to(torch.float32).contiguous()
-    if rows is not None and (rows.shape != shape or rows.dtype != torch.bfloat16 or
-                             not rows.is_contiguous() or rows.get_device() != index):
-        raise ValueError(f"rows must be contiguous bf16 [{n}, {d}] on cuda:{index}")
-    _call(index, lib().mla_cache_append, kv.data_ptr(), max(stride, d), d, slots.data_ptr(),
-          None if positions is None else positions.data_ptr(),
-          None if norm_gain is None else norm_gain.data_ptr(), eps, rope_base, n,
-          kcache.data_ptr(), kcache.numel() // width, row_bytes,
-          None if rows is None else rows.data_ptr())
-    return rows
+    return (_calls or calls()).cache_append(kv, slots, kcache, positions, norm_gain, eps,
+                                            rope_base, rows)

@@ -1,4 +1,5 @@
-"""Build libmla_b200.so in-tree with nvcc for sm_100a.
+"""Build libmla_b200.so (nvcc, sm_100a) and _torch_calls.so (the extension module
+that takes the cache-side calls from Python to it) in-tree.
 
     python -m mla_paged_kv_03_b200.build [--force]
 
@@ -11,6 +12,7 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -32,17 +34,45 @@ FLAGS = [
 ]
 
 
-def _stale():
-    if not os.path.exists(LIB):
+CALLS = os.path.join(HERE, "_torch_calls.so")
+CALLS_DEPS = [os.path.join(CSRC, "torch_calls.cpp"), os.path.join(ROOT, "include", "mla.h")]
+
+
+def _stale(target=LIB, deps=DEPS):
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(d) > t for d in DEPS)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(d) > t for d in deps)
+
+
+def build_calls(force: bool = False) -> str:
+    """Compile _torch_calls.so against the installed torch and libmla_b200.so."""
+    if not force and not _stale(CALLS, CALLS_DEPS):
+        return CALLS
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden", "-Wall", "-Wno-unknown-pragmas",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-o", CALLS, CALLS_DEPS[0],
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("building _torch_calls.so failed")
+    return CALLS
 
 
 def build(force: bool = False, verbose: bool = False, out: str = None, defines=()) -> str:
     """Compile libmla_b200.so (or `out`, with extra -D `defines`)."""
     target = out or LIB
     if not force and not defines and out is None and not _stale():
+        build_calls()
         return LIB
     cmd = [NVCC] + FLAGS + [f"-D{d}" for d in defines] + \
         ["-I", os.path.join(ROOT, "include"), "-o", target] + SOURCES + ["-lcudart"]
@@ -63,6 +93,7 @@ def build(force: bool = False, verbose: bool = False, out: str = None, defines=(
     if out is None:
         with open(os.path.join(HERE, "ptxas_report.txt"), "w") as f:
             f.write(log)
+        build_calls(force)
     return target
 
 

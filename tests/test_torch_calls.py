@@ -1,0 +1,50 @@
+"""Argument checks of the cache-side calls that need no GPU: CPU tensors, other
+objects and wrong counts are refused with a Python error."""
+import pytest
+import torch
+
+from mla_paged_kv_03_b200 import binding as B
+
+BF16 = torch.bfloat16
+
+
+def append_args(**o):
+    a = dict(kv=torch.zeros((4, 576), dtype=BF16), slots=torch.zeros(4, dtype=torch.int32),
+             kcache=torch.zeros((2, 64, 1, 576), dtype=BF16))
+    return a | o
+
+
+def test_cpu_tensors_are_refused():
+    cache = torch.zeros((2, 64, 1, 576), dtype=BF16)
+    q = torch.zeros((1, 1, 16, 576), dtype=BF16)
+    i32 = torch.zeros((1, 2), dtype=torch.int32)
+    sl = torch.zeros(1, dtype=torch.int32)
+    keys, scales = torch.zeros((2, 576), dtype=torch.int8), torch.zeros(2)
+    with pytest.raises(ValueError, match="kv must be CUDA"):
+        B.mla_cache_append(**append_args())
+    with pytest.raises(ValueError, match="kcache"):
+        B.mla_page_keys_update(cache, i32, sl, keys, scales)
+    with pytest.raises(ValueError, match="q must be CUDA"):
+        B.mla_page_sparse_decode(q, cache, keys, scales, i32, sl, 2)
+    with pytest.raises(ValueError, match="q must be CUDA"):
+        B.mla_shared_prefix_decode_fwd(q, cache, sl, 64, i32, sl, i32, sl, 4)
+
+
+@pytest.mark.parametrize("over", [
+    dict(kv=None), dict(kv=[1, 2]), dict(kcache=None), dict(kcache="cache"),
+    dict(kcache=torch.zeros((2, 64, 512), dtype=BF16)),
+    dict(kcache=torch.zeros((2, 64, 600), dtype=torch.uint8)),
+    dict(kcache=torch.zeros((), dtype=BF16)),
+    dict(kv=torch.zeros((4, 512), dtype=BF16)), dict(kv=torch.zeros((4, 576)))])
+def test_other_objects_and_shapes_are_refused(over):
+    with pytest.raises(ValueError):
+        B.mla_cache_append(**append_args(**over))
+
+
+def test_counts_of_arguments():
+    for f in (B.calls().cache_append, B.calls().page_keys_update, B.calls().page_sparse_decode,
+              B.calls().shared_prefix_decode):
+        with pytest.raises(TypeError):
+            f()
+        with pytest.raises(TypeError):
+            f(*[None] * 30)
