@@ -46,7 +46,7 @@ namespace mla {
 
 constexpr int kRow1152 = 2 * kD;  // bf16 cache row
 constexpr int kAppendWarps = 8;
-constexpr int kAppendCtas = 4;  // CTAs per SM of a full grid
+constexpr int kAppendCtas = 5;  // CTAs per SM of a full grid
 
 struct AppendParams {
   const __nv_bfloat16* kv;  // [n] rows of d values, kv_stride values apart
@@ -177,11 +177,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const double turns = P.turns[lane];
-  float g[2][8];
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) g[j][e] = P.gain ? __ldg(P.gain + (lane + 32 * j) * 8 + e) : 1.f;
+  __shared__ __align__(16) float s_gain[kNope];
+  if (P.gain) {
+    for (int i = threadIdx.x; i < kNope; i += 32 * kAppendWarps) s_gain[i] = __ldg(P.gain + i);
+    __syncthreads();
+  }
 
   for (long long t = (long long)blockIdx.x * kAppendWarps + warp; t < P.n;
        t += (long long)gridDim.x * kAppendWarps) {
@@ -224,9 +224,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
                              : inv_root_by_fp64(raw[0], raw[1], P.eps);
       const float inv32 = static_cast<float>(inv);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j) {
+        const float4* g = reinterpret_cast<const float4*>(s_gain + (lane + 32 * j) * 8);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[j][e] *= g[j][e] * inv32;
+        for (int e = 0; e < 2; ++e) {
+          const float4 f = g[e];
+          y[j][4 * e] *= f.x * inv32;
+          y[j][4 * e + 1] *= f.y * inv32;
+          y[j][4 * e + 2] *= f.z * inv32;
+          y[j][4 * e + 3] *= f.w * inv32;
+        }
+      }
     }
     if (P.positions) {
       if (kWide)
