@@ -137,6 +137,9 @@ MLA_API int mla_fused_workspace_size(int batch, int h_q, int num_sm_parts, size_
  *                   cache_seqlens and heads_per_kv = s_q*h_q
  *   workspace       device scratch of >= mla_workspace_size() bytes,
  *                   16-byte aligned; contents need no initialisation
+ * Cache rows behind a sequence's tokens may hold anything, NaN included; the
+ * rows of its tokens must be finite (one that a query does not see enters its
+ * sums with weight zero).
  * Launches the decode kernel and the split-combine kernel on `stream`. */
 MLA_API int mla_decode_fwd(const void* q, const void* kcache, const int32_t* block_table, int max_pages,
                    int num_blocks, const int32_t* cache_seqlens, int batch, int s_q, int h_q,
@@ -312,9 +315,8 @@ MLA_API int mla_sparse_fused_norm_rope_attn_rope_cast(
  *                 for the same cache_seqlens, rows_per_kv = s_q * h_q and
  *                 prefix_len; num_sm_parts from mla_num_sm_parts(device, 128,
  *                 1).  Sizes from mla_shared_prefix_metadata_size.  A plan of
- *                 another batch, row count or prefix presence is not run: it
- *                 sets the bad-index status and leaves out and lse as they
- *                 were
+ *                 other row groups or another prefix_len is not run: it sets
+ *                 the bad-index status and leaves out and lse as they were
  *   workspace     >= mla_shared_prefix_workspace_size() bytes, 16-byte aligned
  * At most 8192 groups of 128 query rows (over the prefix plus over own
  * tokens).  Other arguments, ownership and errors as in mla_decode_fwd; a
@@ -346,7 +348,9 @@ MLA_API int mla_shared_prefix_decode_fwd(const void* q, const void* kcache, int 
  *   code = m / scale rounded to the nearest, ties to even
  * Recomputes the last `tail_pages` pages of every sequence (all of them where
  * it has fewer).  After appending n tokens to each sequence, tail_pages =
- * ceil(n / 64) + 1 covers every page that changed.
+ * ceil(n / 64) + 1 covers every page that changed.  A block that several
+ * sequences name gets one key: it must hold as many rows in each of them.  The
+ * rows must be finite.
  *   kcache, num_blocks, block_table, max_pages, cache_seqlens: as in
  *                 mla_decode_fwd, the lengths after the append
  *   page_keys     int8[num_blocks][576], 16-byte aligned; page_scales

@@ -39,6 +39,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <climits>
 #include <cstdint>
 
 #include "mla_common.h"
@@ -282,6 +283,19 @@ __device__ __forceinline__ int clamp_block(int blk, int num_blocks) {
   return blk;
 }
 
+// A token past a sequence's end enters PV with P = 0, which leaves O alone only
+// if its row is finite, and the cache may hold anything there.  So a page of
+// which the sequence has n < 64 rows is loaded from its row n - 64 on: TMA fills
+// the rows before the page's first with zeros, the n rows follow, and none behind
+// them is read.  Slot t of such a page is token t - page_shift of the page, and
+// no token for t < page_shift.  (The maps have the rows of a page in a dimension
+// of their own, so that rows -64 .. -1 are outside of it.)
+// 0 for a page that the sequence does not reach, which is masked whole.
+__device__ __forceinline__ int page_shift(int L, int page) {
+  const int n = L - page * kPage;
+  return n > 0 && n < kPage ? kPage - n : 0;
+}
+
 // --------------------------------------------------------------------------
 template <int kMode>
 __global__ void __launch_bounds__(Threads<kMode>::value, 1)
@@ -376,6 +390,9 @@ __global__ void __launch_bounds__(Threads<kMode>::value, 1)
       int blk1 = (p0 + 1 < npg) ? P.block_table[(size_t)un.b * P.max_pages + p0 + 1] : blk0;
       blk0 = clamp_block(blk0, P.num_blocks);
       blk1 = clamp_block(blk1, P.num_blocks);
+      // an empty sequence loads zeros
+      const int y0 = un.L > 0 ? -page_shift(un.L, p0) : -kPage;
+      const int y1 = p0 + 1 < npg ? -page_shift(un.L, p0 + 1) : y0;
       if (P.trace && pair == 0) {
         if (p0 < npg) trace_page(P, un.b, p0, blk0, planes);
         if (p0 + 1 < npg) trace_page(P, un.b, p0 + 1, blk1, planes);
@@ -385,9 +402,9 @@ __global__ void __launch_bounds__(Threads<kMode>::value, 1)
         uint8_t* dst = sRing + slot * kPairBytes;
         for (int j = 0; j < nch; ++j) {
           const int x = (c0 + j) * kChunkD;
-          ptx::tma_load_2d(dst + j * kSubChunk, &tm_kv, &C.slot_full[slot], x, blk0 * kPage);
-          ptx::tma_load_2d(dst + j * kSubChunk + kSubChunk / 2, &tm_kv, &C.slot_full[slot], x,
-                           blk1 * kPage);
+          ptx::tma_load_3d(dst + j * kSubChunk, &tm_kv, &C.slot_full[slot], x, y0, blk0);
+          ptx::tma_load_3d(dst + j * kSubChunk + kSubChunk / 2, &tm_kv, &C.slot_full[slot], x, y1,
+                           blk1);
         }
       }
       __syncwarp();
@@ -604,7 +621,8 @@ __global__ void __launch_bounds__(Threads<kMode>::value, 1)
         ptx::mbar_arrive(&C.s_empty[sb]);
 
         const int tile_tok0 = (u.lo + k) * kTileT;
-        const int T = tile_tok0 + t;
+        const int shift = page_shift(u.L, 2 * (u.lo + k) + t / kPage);
+        const int T = t % kPage < shift ? INT_MAX : tile_tok0 + t - shift;
         const bool need_mask = tile_tok0 + kTileT > min_lim;
         int need = 0;
 #pragma unroll

@@ -126,6 +126,29 @@ int make_latent_map3(CUtensorMap* map, const void* base, long long rows, int box
   return MLA_OK;
 }
 
+// Views of a paged cache with the rows of a page in a dimension of their own, so
+// that a load from a negative row of a page reads zeros there: [576 dims][64
+// rows][block] with boxes of 64 dims of one page, and, for 2 `chunks` of 64 dims
+// in one box, [64 dims][64 rows][9 chunks][block].
+int make_page_map(CUtensorMap* map, const void* kcache, int num_blocks, int chunks = 0) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t row = mla::kD * 2, blocks = static_cast<cuuint64_t>(num_blocks);
+  cuuint64_t dims3[3] = {mla::kD, mla::kPage, blocks};
+  cuuint64_t strides3[2] = {row, row * mla::kPage};
+  cuuint32_t box3[3] = {mla::kChunkD, mla::kPage, 1};
+  cuuint64_t dims4[4] = {mla::kChunkD, mla::kPage, mla::kNumChunks, blocks};
+  cuuint64_t strides4[3] = {row, mla::kChunkD * 2, row * mla::kPage};
+  cuuint32_t box4[4] = {mla::kChunkD, mla::kPage, static_cast<cuuint32_t>(chunks), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, chunks ? 4 : 3, const_cast<void*>(kcache),
+                  chunks ? dims4 : dims3, chunks ? strides4 : strides3, chunks ? box4 : box3, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled (pages) failed (%d)", (int)r);
+  return MLA_OK;
+}
+
 struct WsLayout {
   size_t o_off, lse_off, q_off, total;
 };
@@ -340,8 +363,7 @@ int launch_pair_decode(const void* q, const void* kcache, const CUtensorMap& tkv
   if (rc != MLA_OK) return rc;
   if (kGather)
     tv3 = tkv;
-  else if ((rc = make_latent_map3(&tv3, kcache, static_cast<long long>(p.num_blocks) * mla::kPage,
-                                  2)) != MLA_OK)
+  else if ((rc = make_page_map(&tv3, kcache, p.num_blocks, 2)) != MLA_OK)
     return rc;
   MLA_CUDA((allow_smem<mla::mla_pair_decode_kernel<kGather, kShared>>(mla::pcfg::kSmemBytes)));
   PdlLaunch L(dim3(static_cast<unsigned>(2 * p.num_parts * p.n_groups)), dim3(mla::pcfg::kThreads),
@@ -781,9 +803,7 @@ int mla_decode_fwd(const void* q, const void* kcache, const int32_t* block_table
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
   CUtensorMap tkv;
-  if ((rc = make_latent_map(&tkv, kcache, static_cast<long long>(num_blocks) * mla::kPage)) !=
-      MLA_OK)
-    return rc;
+  if ((rc = make_page_map(&tkv, kcache, num_blocks)) != MLA_OK) return rc;
 
   mla::DecodeParams p{};
   p.batch = batch;
@@ -865,9 +885,7 @@ int mla_fused_norm_rope_attn_rope_cast(
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
   CUtensorMap tkv;
-  if ((rc = make_latent_map(&tkv, kcache, static_cast<long long>(num_blocks) * mla::kPage)) !=
-      MLA_OK)
-    return rc;
+  if ((rc = make_page_map(&tkv, kcache, num_blocks)) != MLA_OK) return rc;
 
   mla::DecodeParams p{};
   p.batch = batch;
@@ -1212,9 +1230,7 @@ int mla_shared_prefix_decode_fwd(const void* q, const void* kcache, int num_bloc
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
   CUtensorMap tkv;
-  if ((rc = make_latent_map(&tkv, kcache, static_cast<long long>(num_blocks) * mla::kPage)) !=
-      MLA_OK)
-    return rc;
+  if ((rc = make_page_map(&tkv, kcache, num_blocks)) != MLA_OK) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   mla::DecodeParams p{};
   p.batch = su.units;
@@ -1248,6 +1264,7 @@ int mla_shared_prefix_decode_fwd(const void* q, const void* kcache, int num_bloc
 
   mla::SharedCombineParams c{};
   c.units = su.units;
+  c.prefix_len = prefix_len;
   c.n_prefix = su.n_prefix;
   c.own_groups = su.own_groups;
   c.R = p.R;

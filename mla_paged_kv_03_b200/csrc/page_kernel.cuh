@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(PageCfg::kThreads, 1)
         const int blk =
             clamp_block(P.block_table[(size_t)u.b * P.max_pages + p0 + k], P.num_blocks);
         if (P.trace && role == 0) trace_page(P, u.b, p0 + k, blk, 3);  // a slot serves K and V
+        const int y = -page_shift(u.L, p0 + k);
         for (int j = 0; j < 5 && ok; ++j) {
           const bool mine = static_cast<int>(item++ & 1) == role;
           if (j < 4) {
@@ -204,8 +205,8 @@ __global__ void __launch_bounds__(PageCfg::kThreads, 1)
             if (ptx::elect_one_sync()) {
               uint8_t* dst = sPair + s * kPairBytes;
               ptx::mbar_arrive_expect_tx(&C.pair_full[s], kPairBytes);
-              ptx::tma_load_2d(dst, &tm_kv, &C.pair_full[s], 128 * j, blk * kPage);
-              ptx::tma_load_2d(dst + kChunk, &tm_kv, &C.pair_full[s], 128 * j + 64, blk * kPage);
+              ptx::tma_load_3d(dst, &tm_kv, &C.pair_full[s], 128 * j, y, blk);
+              ptx::tma_load_3d(dst + kChunk, &tm_kv, &C.pair_full[s], 128 * j + 64, y, blk);
             }
             __syncwarp();
           } else {
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(PageCfg::kThreads, 1)
             }
             if (ptx::elect_one_sync()) {
               ptx::mbar_arrive_expect_tx(&C.rope_full[s], kChunk);
-              ptx::tma_load_2d(sRope + s * kChunk, &tm_kv, &C.rope_full[s], kNope, blk * kPage);
+              ptx::tma_load_3d(sRope + s * kChunk, &tm_kv, &C.rope_full[s], kNope, y, blk);
             }
             __syncwarp();
           }
@@ -458,7 +459,8 @@ __global__ void __launch_bounds__(PageCfg::kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&C.s_empty[sb]);
 
-        const int T = (p0 + k) * kPage + t;
+        const int shift = page_shift(u.L, p0 + k);
+        const int T = t < shift ? INT_MAX : (p0 + k) * kPage + t - shift;
         const bool need_mask = (p0 + k + 1) * kPage > min_lim;
         int need = 0;
 #pragma unroll

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
   constexpr Mode kUnits = kShared ? kSharedPrefix : kDense;
   if constexpr (kShared) {
     // a plan made for other units names none of these: leave (both CTAs alike)
-    if (meta[5] != P.batch) {
+    if (meta[5] != P.batch || meta[6] != P.prefix_len) {
       if (threadIdx.x == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x47);
       return;
     }
@@ -212,6 +212,12 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
     }
     const int blk = pg < npg ? table[pg] : 0;
     return clamp_block(blk, P.num_blocks);
+  };
+  // First row of the load of logical page `page`, or of the page that stands in
+  // for it (page_shift; an empty sequence loads zeros).
+  auto page_row0 = [&](const Unit& un, int page, int fallback) -> int {
+    const int end = min((un.L + kPage - 1) / kPage, 2 * un.hi);
+    return un.L > 0 ? -page_shift(un.L, page < end ? page : fallback) : -kPage;
   };
   // Gather mode: the row of index entry e of unit `un` (row 0, masked, for an
   // entry past the unit's length or naming no row).
@@ -294,6 +300,8 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
       const int p0 = 2 * (un.lo + 2 * i);
       const int kb0 = page_block(un, p0 + 2 * static_cast<int>(rank), p0);
       const int kb1 = page_block(un, p0 + 2 * static_cast<int>(rank) + 1, p0);
+      const int ky0 = page_row0(un, p0 + 2 * static_cast<int>(rank), p0);
+      const int ky1 = page_row0(un, p0 + 2 * static_cast<int>(rank) + 1, p0);
       if (P.trace && role == 0) {
         trace_if_real(un, p0 + 2 * static_cast<int>(rank), kb0, 1);
         trace_if_real(un, p0 + 2 * static_cast<int>(rank) + 1, kb1, 1);
@@ -307,8 +315,8 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
           if (leader) ptx::mbar_arrive_expect_tx(&C.full[s], 2u * kStage);
           const uint32_t bar = leader_addr(&C.full[s]);
           uint8_t* dst = sRing + s * kStage;
-          ptx::tma_load_2d_pair(dst, &tm_kv, bar, c * kChunkD, kb0 * kPage);
-          ptx::tma_load_2d_pair(dst + kBox, &tm_kv, bar, c * kChunkD, kb1 * kPage);
+          ptx::tma_load_3d_pair(dst, &tm_kv, bar, c * kChunkD, ky0, kb0);
+          ptx::tma_load_3d_pair(dst + kBox, &tm_kv, bar, c * kChunkD, ky1, kb1);
         }
         __syncwarp();
       }
@@ -345,9 +353,12 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
         return true;
       }
       const int p0 = 2 * (un.lo + 2 * i);
-      int vb[4];
+      int vb[4], vy[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) vb[q] = page_block(un, p0 + q, p0);
+      for (int q = 0; q < 4; ++q) {
+        vb[q] = page_block(un, p0 + q, p0);
+        vy[q] = page_row0(un, p0 + q, p0);
+      }
       if (P.trace && role == 0)
         for (int q = 0; q < 4; ++q) trace_if_real(un, p0 + q, vb[q], 2);
       for (int j = 0; j < 2; ++j)
@@ -358,8 +369,8 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
           if (!mine) continue;
           if (ptx::elect_one_sync()) {
             if (leader) ptx::mbar_arrive_expect_tx(&C.full[s], 2u * kStage);
-            ptx::tma_load_3d_pair(sRing + s * kStage, &tm_v3, leader_addr(&C.full[s]), 0,
-                                  vb[q] * kPage, 4 * j + 2 * static_cast<int>(rank));
+            ptx::tma_load_4d_pair(sRing + s * kStage, &tm_v3, leader_addr(&C.full[s]), 0, vy[q],
+                                  4 * j + 2 * static_cast<int>(rank), vb[q]);
           }
           __syncwarp();
         }
@@ -579,7 +590,15 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t s_addr = lane_addr + kSCol + sb * 128 + 64 * wg;
-        const int nvalid = lim - ((u.lo + 2 * i) * kTileT + 64 * quarter);
+        // The quarter is one page, of whose slots [shift, nvalid) are tokens that
+        // the row sees; those before are masked by a score of -inf, which is
+        // well-defined since nvalid > shift then.
+        int nvalid = lim - ((u.lo + 2 * i) * kTileT + 64 * quarter);
+        int shift = 0;
+        if constexpr (!kGather) {
+          shift = page_shift(u.L, 2 * u.lo + 4 * i + quarter);
+          nvalid = nvalid > 0 ? nvalid + shift : 0;
+        }
         // One pass with the running maximum m: P = 2^(scale*s - m).  When some
         // row's maximum exceeds m_used by more than the threshold (always on a
         // unit's first step), all softmax warps redo the pass with the new
@@ -599,6 +618,10 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
           for (int cc = 0; cc < 2; ++cc) {
             float* x = cc ? xb : xa;
             if (cc) ptx::tmem_ld_wait_regs(xb);
+            if (!kGather && shift > 32 * cc) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = 32 * cc + j < shift ? -INFINITY : x[j];
+            }
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
               const bool v0 = 32 * cc + j < nvalid && ((vmask[cc] >> j) & 1u);

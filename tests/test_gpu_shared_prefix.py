@@ -235,6 +235,30 @@ def test_a_plan_of_other_units_is_refused_on_the_device():
     c.check(c.run())
 
 
+def test_a_plan_of_another_prefix_length_is_refused_on_the_device():
+    c = Case([70, 64], 130, 1, 16, seed=13)
+    q, cache, pt, table, sl = c.dev()
+    meta, ns, n = B.mla_shared_prefix_get_metadata(sl, 64, 16)
+    out = torch.full((2, 1, 16, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    B.mla_shared_prefix_decode_fwd(q, cache, pt, 130, table, sl, meta, ns, n, out=out)
+    assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+    assert (out == 3.0).all()
+    c.check(c.run())
+
+
+def test_rejects_outputs_and_workspaces_of_other_shapes():
+    c = Case([70, 64], 130, 1, 16, seed=13)
+    for bad in (dict(out=torch.empty((2, 1, 15, 512), dtype=torch.bfloat16, device="cuda")),
+                dict(out=torch.empty((2, 1, 16, 512), device="cuda")),
+                dict(out=torch.empty((2, 1, 16, 1024), dtype=torch.bfloat16,
+                                     device="cuda")[..., ::2]),
+                dict(lse=torch.empty((2, 16), device="cuda")),
+                dict(lse=torch.empty((2, 1, 16))),
+                dict(workspace=torch.empty(1 << 24, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            c.run(**bad)
+
+
 def test_slot_trace_names_the_rows_read():
     c = Case([70, 200], 130, 1, 16, seed=14)
     width = c.table.shape[1]
