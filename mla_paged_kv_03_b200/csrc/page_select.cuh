@@ -50,17 +50,18 @@ struct PageKeysParams {
 };
 
 constexpr int kKeyUnits = kD / 8;      // 16-byte units of a row
-constexpr int kKeyRowGroups = 8;       // threads that share a unit, each every 8th row
-constexpr int kKeySummers = kKeyUnits * kKeyRowGroups;  // 576 threads: also one per dim
-constexpr int kKeyThreads = kKeySummers + 32;           // and a warp that fetches
+constexpr int kKeyRowGroups = 4;       // threads that share a unit, each every 4th row
+constexpr int kKeyGroup = kKeyUnits * kKeyRowGroups;  // 288 threads sum a page: two dims each
+constexpr int kKeyGroups = 2;                         // groups, with every second page
+constexpr int kKeyThreads = kKeyGroups * kKeyGroup + 32;  // and a warp that fetches
 constexpr int kKeyHalf = kPage / 2;    // rows of a stage
-constexpr int kKeyStages = 4;
 constexpr int kKeyStageBytes = kKeyHalf * kD * 2;  // 36864
-// Partial sums: [row group][pair of a unit's dims][unit] two doubles, a pair's
-// units padded so that neither the stores (a thread per unit) nor the loads (a
-// thread per dim) meet in a bank more than twice.
+// Partial sums of a group: [row group][pair of a unit's dims][unit] two doubles,
+// a pair's units padded so that neither the stores (a thread per unit) nor the
+// loads (a thread per pair) meet in a bank more than twice.
 constexpr int kKeyPairStride = kKeyUnits + 4;
-constexpr int kKeySmem = kKeyStages * kKeyStageBytes + kKeyRowGroups * 4 * kKeyPairStride * 16;
+constexpr int kKeySumBytes = kKeyRowGroups * 4 * kKeyPairStride * 16;
+constexpr int kKeySmem = kKeyGroups * (2 * kKeyStageBytes + kKeySumBytes);
 
 // Untiled bulk copy of `bytes` (a multiple of 16) to this CTA's shared memory.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
@@ -70,6 +71,20 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
           "r"(ptx::smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
       : "memory");
+}
+
+// All of the threads of group g of the page key kernel have ok (uniform).
+__device__ __forceinline__ bool key_group_and(int g, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1 : 0), "r"(1 + g), "n"(kKeyGroup)
+      : "memory");
+  return all != 0;
 }
 
 // The two bf16 values of a word as the high words of doubles, 2^896 times too
@@ -82,137 +97,152 @@ __device__ __forceinline__ double high_bf16_scaled(uint32_t w) {
   return __hiloint2double((static_cast<int>(w) >> 3) & 0x8FFFE000, 0);
 }
 
-// One CTA per SM goes over the (page, sequence) places tail * batch, page by
-// page.  The rows of a page that the sequence has lie in one piece, which comes
-// in by bulk copies of 32 rows into four stages, so that two pages are in
-// flight while one is summed; a warp of its own looks up the next page behind
-// the sums.  The sums are formed in fp64, where 64 bf16 values add exactly
-// unless they lie 39 binades apart: the code does not depend on the order, and
-// a mean next to a rounding border is decided by its value.  Converting bf16 to
-// fp64 at the conversion unit's rate (16 a clock per SM) costs more than the
-// page's share of HBM time; placing the bits does not.
+// One CTA per SM goes over the (page, sequence) places tail * batch.  Two groups
+// of 288 threads take every second page each, so that one group's reduction and
+// waits lie behind the other's sums; a warp of its own looks up the pages and
+// fetches them.  The rows of a page that the sequence has lie in one piece, which
+// comes in by bulk copies of 32 rows.  The sums are formed in fp64, where 64 bf16
+// values add exactly unless they lie 39 binades apart: the code does not depend
+// on the order, and a mean next to a rounding border is decided by its value.
+// Converting bf16 to fp64 at the conversion unit's rate (16 a clock per SM) costs
+// more than the page's share of HBM time; placing the bits does not.
+// HBM bound; 6144 pages (453 MB) on B200: 135 us with a CTA per page and
+// conversions, 117 us with bulk copies, 86 us with bits placed, 76 us with two
+// groups; the copies alone take 73 us.
 __global__ void __launch_bounds__(kKeyThreads, 1) mla_page_keys_kernel(const PageKeysParams P) {
   extern __shared__ __align__(128) uint8_t s_buf[];
-  __shared__ uint64_t s_full[kKeyStages];
-  __shared__ uint32_t s_max[kKeySummers / 32];
-  __shared__ int s_blk[kKeyStages], s_rows[kKeyStages];  // of the pages in flight; 0 rows: none
-  double2* s_sum = reinterpret_cast<double2*>(s_buf + kKeyStages * kKeyStageBytes);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool fetcher = tid == kKeySummers;
-  const bool summer = tid < kKeySummers;
-  if (fetcher) {
-    for (int i = 0; i < kKeyStages; ++i) ptx::mbar_init(&s_full[i], 1);
+  __shared__ uint64_t s_full[kKeyGroups][2], s_empty[kKeyGroups];  // [group][half of the page]
+  __shared__ uint32_t s_max[kKeyGroups][kKeyGroup / 32];
+  __shared__ int s_blk[kKeyGroups], s_rows[kKeyGroups];  // the group's page; 0 rows: the end
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) {
+    for (int g = 0; g < kKeyGroups; ++g) {
+      ptx::mbar_init(&s_full[g][0], 1);
+      ptx::mbar_init(&s_full[g][1], 1);
+      ptx::mbar_init(&s_empty[g], kKeyGroup / 32);
+    }
     ptx::fence_mbar_init();
   }
   __syncthreads();
-  // the fetcher's state: the next place, its block and rows
-  const long long items = static_cast<long long>(P.tail) * P.batch;
-  long long item = blockIdx.x;
-  int fetched = 0, next_rows = 0, next_blk = 0;
-  auto locate = [&]() {  // the next place that holds a page
-    next_rows = 0;
-    for (; next_rows == 0 && item < items; item += gridDim.x) {
-      const int b = static_cast<int>(item / P.tail);
-      int L = P.seqlens[b];
-      if (L > P.max_pages * kPage) {
-        ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x72);
-        L = P.max_pages * kPage;
+
+  if (tid >= kKeyGroups * kKeyGroup) {
+    if (lane != 0) return;
+    const long long items = static_cast<long long>(P.tail) * P.batch;
+    long long item = blockIdx.x;
+    for (int k = 0;; ++k) {  // page k of this CTA goes to group k % 2
+      int rows = 0, blk = 0;
+      for (; rows == 0 && item < items; item += gridDim.x) {
+        const int b = static_cast<int>(item / P.tail);
+        int L = P.seqlens[b];
+        if (L > P.max_pages * kPage) {
+          ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x72);
+          L = P.max_pages * kPage;
+        }
+        const int page = (L + kPage - 1) / kPage - P.tail +
+                         static_cast<int>(item - static_cast<long long>(b) * P.tail);
+        if (L <= 0 || page < 0) continue;
+        rows = min(kPage, L - page * kPage);
+        blk = clamp_block(P.block_table[static_cast<size_t>(b) * P.max_pages + page],
+                          P.num_blocks);
       }
-      const int page = (L + kPage - 1) / kPage - P.tail +
-                       static_cast<int>(item - static_cast<long long>(b) * P.tail);
-      if (L <= 0 || page < 0) continue;
-      next_rows = min(kPage, L - page * kPage);
-      next_blk = clamp_block(P.block_table[static_cast<size_t>(b) * P.max_pages + page],
-                             P.num_blocks);
-    }
-  };
-  auto fetch = [&]() {  // its copies, into the stages of page `fetched`
-    const __nv_bfloat16* src = P.kcache + static_cast<size_t>(next_blk) * kPage * kD;
-    s_blk[fetched % kKeyStages] = next_blk;
-    s_rows[fetched % kKeyStages] = next_rows;
-    if (next_rows == 0) return;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int st = (2 * fetched + h) % kKeyStages;
-      const int rows = min(kKeyHalf, next_rows - h * kKeyHalf);
-      if (rows > 0) {
-        ptx::mbar_arrive_expect_tx(&s_full[st], rows * kD * 2);
-        bulk_load(s_buf + st * kKeyStageBytes, src + h * kKeyHalf * kD, rows * kD * 2,
-                  &s_full[st]);
-      } else {
-        ptx::mbar_arrive(&s_full[st]);
+      const int g = k % kKeyGroups, round = k / kKeyGroups;
+      // the group is done with its last page (and so are the copies of it)
+      if (!ptx::mbar_wait(&s_empty[g], (round & 1) ^ 1, 0x74)) {
+        // give up, once the other group's copies have landed (bounded, too)
+        if (k > 0) {
+          const int o = (k - 1) % kKeyGroups, ro = (k - 1) / kKeyGroups;
+          ptx::mbar_wait(&s_full[o][0], ro & 1, 0x75);
+          ptx::mbar_wait(&s_full[o][1], ro & 1, 0x75);
+        }
+        return;
       }
-    }
-    ++fetched;
-  };
-  if (fetcher)
-    for (int i = 0; i < kKeyStages / 2; ++i) {
-      locate();
-      fetch();
-    }
-  __syncthreads();
-  const int unit = tid % kKeyUnits, group = tid / kKeyUnits;
-  for (int done = 0;; ++done) {
-    const int n = s_rows[done % kKeyStages], blk = s_blk[done % kKeyStages];
-    if (n == 0) return;
-    bool ok = true;
-    if (fetcher) locate();
-    if (summer) {
-      double sum[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] = 0.0;
+      s_blk[g] = blk;
+      s_rows[g] = rows;
+      const __nv_bfloat16* src = P.kcache + static_cast<size_t>(blk) * kPage * kD;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int st = (2 * done + h) % kKeyStages;
-        ok = ptx::mbar_wait(&s_full[st], (done / (kKeyStages / 2)) & 1, 0x74) && ok;
-        const uint4* src = reinterpret_cast<const uint4*>(s_buf + st * kKeyStageBytes) + unit;
+        const int n = min(kKeyHalf, rows - h * kKeyHalf);
+        if (n > 0) {
+          ptx::mbar_arrive_expect_tx(&s_full[g][h], n * kD * 2);
+          bulk_load(s_buf + (2 * g + h) * kKeyStageBytes, src + h * kKeyHalf * kD, n * kD * 2,
+                    &s_full[g][h]);
+        } else {
+          ptx::mbar_arrive(&s_full[g][h]);
+        }
+      }
+      // after the last page each group gets an end mark
+      if (rows == 0 && k >= kKeyGroups - 1 && s_rows[(k + 1) % kKeyGroups] == 0) return;
+    }
+  }
+
+  const int g = tid / kKeyGroup, t = tid - g * kKeyGroup, warp = t >> 5;
+  const int unit = t % kKeyUnits, row_group = t / kKeyUnits;
+  double2* s_sum = reinterpret_cast<double2*>(s_buf + 2 * kKeyGroups * kKeyStageBytes +
+                                              g * kKeySumBytes);
+  for (int round = 0;; ++round) {
+    if (!key_group_and(g, ptx::mbar_wait(&s_full[g][0], round & 1, 0x76))) break;
+    const int n = s_rows[g], blk = s_blk[g];
+    if (n == 0) return;
+    bool ok = true;
+    double sum[8];
 #pragma unroll
-        for (int i = 0; i < kKeyHalf / kKeyRowGroups; ++i) {
-          const int row = group + kKeyRowGroups * i;
-          if (h * kKeyHalf + row < n) {
-            const uint4 w = src[row * kKeyUnits];
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    for (int e = 0; e < 8; ++e) sum[e] = 0.0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              sum[2 * e] += low_bf16_scaled(u[e]);
-              sum[2 * e + 1] += high_bf16_scaled(u[e]);
-            }
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1) ok = ptx::mbar_wait(&s_full[g][1], round & 1, 0x77);
+      const uint4* src = reinterpret_cast<const uint4*>(s_buf + (2 * g + h) * kKeyStageBytes) + unit;
+#pragma unroll
+      for (int i = 0; i < kKeyHalf / kKeyRowGroups; ++i) {
+        const int row = row_group + kKeyRowGroups * i;
+        if (h * kKeyHalf + row < n) {
+          const uint4 w = src[row * kKeyUnits];
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum[2 * e] += low_bf16_scaled(u[e]);
+            sum[2 * e + 1] += high_bf16_scaled(u[e]);
           }
         }
       }
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&s_empty[g]);  // the page was read: fetch the next
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        s_sum[(group * 4 + e) * kKeyPairStride + unit] = make_double2(sum[2 * e], sum[2 * e + 1]);
-    }
-    if (!__syncthreads_and(ok)) {  // a copy did not come: wait (bounded) for the others
-      if (fetcher)
-        for (int j = done; j < fetched; ++j)
-          for (int h = 0; h < 2; ++h)
-            ptx::mbar_wait(&s_full[(2 * j + h) % kKeyStages], (j / (kKeyStages / 2)) & 1, 0x75);
-      return;
-    }
-    if (fetcher) fetch();  // into the two stages just read
-    float mean = 0.f;
-    if (summer) {  // dim tid: of pair (tid % 8) / 2 of unit tid / 8
-      double t = 0.0;
+    for (int e = 0; e < 4; ++e)
+      s_sum[(row_group * 4 + e) * kKeyPairStride + unit] = make_double2(sum[2 * e], sum[2 * e + 1]);
+    if (!key_group_and(g, ok)) break;
+    // dims 2 t and 2 t + 1: pair t % 4 of unit t / 4
+    double2 total = make_double2(0.0, 0.0);
 #pragma unroll
-      for (int g = 0; g < kKeyRowGroups; ++g)
-        t += reinterpret_cast<const double*>(
-            s_sum)[((g * 4 + ((tid & 7) >> 1)) * kKeyPairStride + (tid >> 3)) * 2 + (tid & 1)];
-      t *= 0x1p+896;
-      mean = static_cast<float>(n == kPage ? t * (1.0 / kPage) : t / n);
-      // magnitudes of floats order like their bits
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(mean)));
-      if (lane == 0) s_max[warp] = top;
+    for (int r = 0; r < kKeyRowGroups; ++r) {
+      const double2 v = s_sum[(r * 4 + (t & 3)) * kKeyPairStride + (t >> 2)];
+      total.x += v.x;
+      total.y += v.y;
     }
-    __syncthreads();
-    if (summer) {
-      const float scale = int8_scale(__uint_as_float(
-          __reduce_max_sync(0xffffffffu, lane < kKeySummers / 32 ? s_max[lane] : 0u)));
-      P.keys[static_cast<size_t>(blk) * kD + tid] = static_cast<int8_t>(int8_code(mean, scale));
-      if (tid == 0) P.scales[blk] = scale;
+    const double inv = n == kPage ? 0x1p+896 / kPage : 0x1p+896;
+    total.x *= inv;
+    total.y *= inv;
+    if (n != kPage) {
+      total.x /= n;
+      total.y /= n;
     }
+    const float m0 = static_cast<float>(total.x), m1 = static_cast<float>(total.y);
+    // magnitudes of floats order like their bits
+    const uint32_t top = __reduce_max_sync(
+        0xffffffffu, max(__float_as_uint(fabsf(m0)), __float_as_uint(fabsf(m1))));
+    if (lane == 0) s_max[g][warp] = top;
+    ptx::named_bar_sync(1 + g, kKeyGroup);
+    const float scale = int8_scale(__uint_as_float(
+        __reduce_max_sync(0xffffffffu, lane < kKeyGroup / 32 ? s_max[g][lane] : 0u)));
+    char2 code;
+    code.x = static_cast<signed char>(int8_code(m0, scale));
+    code.y = static_cast<signed char>(int8_code(m1, scale));
+    reinterpret_cast<char2*>(P.keys + static_cast<size_t>(blk) * kD)[t] = code;
+    if (t == 0) P.scales[blk] = scale;
   }
+  // a copy did not come in time: leave once those of this group have landed (bounded)
+  for (int h = 0; h < 2; ++h)
+    for (uint32_t parity = 0; parity < 2; ++parity) ptx::mbar_wait(&s_full[g][h], parity, 0x78);
 }
 
 // ------------------------------------------------------------------ selection
