@@ -1399,7 +1399,14 @@ int mla_page_sparse_decode(const void* q, const void* kcache, int num_blocks,
   p.taken_table = table;
   p.taken_lens = lens;
   p.pages = pages;
-  p.num_parts = num_sm_parts;
+  // The queries take about as many pages each: with a whole number of parts per
+  // query no part holds the ends of two of them, each with its own query load and
+  // epilogue.  B200, 128 heads, 32 pages, step us with all 74 parts and with the
+  // whole number: 16 queries 38.2 and 36.1, 20: 46.8 and 41.4, 28: 52.3 and 49.1,
+  // 32: 58.6 and 57.3, 40 (16 pages): 50.2 and 41.9; 64 heads, 32 queries, 148
+  // and 128 parts: 56.1 and 54.2.
+  const int parts = pairs <= num_sm_parts ? num_sm_parts / pairs * pairs : num_sm_parts;
+  p.num_parts = parts;
   p.plan = mla::plan_params(h_q);
   p.metadata = meta;
   p.num_splits = splits;
@@ -1428,7 +1435,7 @@ int mla_page_sparse_decode(const void* q, const void* kcache, int num_blocks,
   cfg.numAttrs = 1;
   MLA_CUDA(cudaLaunchKernelEx(&cfg, mla::mla_page_select_kernel, p));
   return mla_decode_fwd(q, kcache, table, w.width, num_blocks, lens, pairs, 1, h_q, 1, d_v,
-                        softmax_scale, 0, meta, splits, num_sm_parts, ws + w.dense_off,
+                        softmax_scale, 0, meta, splits, parts, ws + w.dense_off,
                         w.dense_bytes, out, lse, stream);
 }
 
