@@ -1411,16 +1411,19 @@ int mla_page_sparse_decode(const void* q, const void* kcache, int num_blocks,
   p.metadata = meta;
   p.num_splits = splits;
   MLA_CUDA(allow_smem<mla::mla_page_select_kernel>(mla::select_smem(mla::kSelHeads, 0)));
-  // CTAs per pair: as many as there are tiles of pages to score, while all of
-  // them still run at once (one per SM)
+  // CTAs per pair: as many as still run at once (one per SM), at most one per 64
+  // pages; tiles of 64 pages if the cluster takes the whole table in one step so
+  // (B200, step us with tiles of 128 and of 64 for 256 pages: 16 queries x 128
+  // heads XXa, 4 x 32 heads XXb; 1024 pages, 32 x 128 heads XXc)
   int dev = 0, sms = 0;
   MLA_CUDA(cudaGetDevice(&dev));
   MLA_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   int cluster = 1;
   if (topk_pages < max_pages)
     while (cluster < mla::kSelMaxCluster && 2 * cluster * (pairs + 1) <= sms &&
-           cluster * mla::kSelTile < max_pages)
+           cluster * (mla::kSelTile / 2) < max_pages)
       cluster *= 2;
+  p.tile = cluster * (mla::kSelTile / 2) >= max_pages ? mla::kSelTile / 2 : mla::kSelTile;
   // an ordinary launch: earlier work of the stream may be writing the inputs
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;

@@ -258,6 +258,7 @@ struct PageSelectParams {
   int pairs, s_q, h_q, causal;
   int topk;                // pages taken (at most)
   int width;               // pages of a taken table row: min(topk, max_pages)
+  int tile;                // pages per step of a CTA: 64 or 128
   uint32_t* scores;        // [pairs, max_pages] order keys >= 1 (scores while heads are left)
   int32_t* taken_table;    // [pairs, width] physical blocks
   int32_t* taken_lens;     // [pairs]
@@ -284,36 +285,33 @@ __device__ __forceinline__ int taken_tokens(const PageSelectParams& P, int seen)
 }
 
 constexpr int kSelThreads = 512;
-constexpr int kSelTile = 64;     // pages per step of a CTA
-constexpr int kSelHeads = 128;   // head rows per pass
-constexpr int kSelStride = kD + 16;  // bytes; an odd number of 16-byte units: no bank conflicts
+constexpr int kSelTile = 128;    // pages per step of a CTA, at most: M of its products
+constexpr int kSelHeads = 128;   // head rows per pass: N of its products, at most
 constexpr int kSelPerThread = 8;     // order keys a thread of the selection holds, at most
 constexpr int kSelMaxCluster = 8;
+constexpr int kSelTmemCols = 128;
 
-// Head rows that a pass of `h_q` heads holds (a warp takes 16).
+// Shared memory of an operand of R rows (pages or heads) of 576 bytes, K-major in
+// the 64-byte swizzle: nine chunks of R x 64 bytes, in a row of which the 16-byte
+// units change places by two bits of the row.  (Pieces of 64 bytes keep the
+// stores to other CTAs few; without swizzle a row lies in pieces of 16.)
+constexpr int kSelChunk = 64;
+constexpr int kSelUnits = kD / 16;  // 36
+__device__ __forceinline__ int sel_offset(int R, int row, int unit) {
+  return (unit >> 2) * R * kSelChunk + row * kSelChunk + (((unit ^ (row >> 1)) & 3) << 4);
+}
+constexpr int kSelKeyBytes = kSelTile * kD;
+
+// Head rows that a pass of `h_q` heads holds (N is a multiple of 16).
 __host__ __device__ inline int select_rows(int h_q) {
   return h_q >= kSelHeads ? kSelHeads : (h_q + 15) / 16 * 16;
 }
 // Dynamic shared memory: the rows' codes and two tiles of keys, or the plan's
 // prefix sums of pairs + 1 costs.
 __host__ __device__ inline int select_smem(int h_q, int pairs) {
-  const int a = (select_rows(h_q) + 2 * kSelTile) * kSelStride, b = (pairs + 1) * 4;
+  const int a = select_rows(h_q) * kD + 2 * kSelKeyBytes + 1024;  // the base aligned
+  const int b = (pairs + 1) * 4;
   return a > b ? a : b;
-}
-
-__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
-__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                       uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -441,11 +439,11 @@ __device__ __forceinline__ void select_block(const uint32_t* keys, const int32_t
 // a cluster of 1..8 CTAs scores the pair's pages and its first CTA selects.
 //   - Each CTA quantises its share of the head rows (128 at a time) and stores
 //     the codes to every CTA of the cluster through distributed shared memory.
-//   - Tiles of 64 pages go round the CTAs.  A tile's keys (37 kB) come in by
-//     cp.async, the next tile's behind this one's products.  A warp keeps the
-//     codes of 16 heads in registers as the A operand and multiplies them with
-//     16 or 32 pages of the tile on the integer tensor cores; the maximum over
-//     the heads goes to the score array as an order key.
+//   - Tiles of 128 pages (64 where the cluster then takes all of them at once) go
+//     round the CTAs.  A tile's keys (at most 74 kB) come in by
+//     cp.async, the next tile's behind this one's products: 18 integer UMMAs of
+//     128 pages x the heads.  A thread then holds a page's products with up to
+//     32 heads; their maximum goes to the score array as an order key.
 //   - The first CTA selects.
 // The keys are 576 bytes a page, 1/128 of the rows they stand for: latency, not
 // bytes, bounds this step, hence one launch for plan, scores and selection, and
@@ -453,7 +451,9 @@ __device__ __forceinline__ void select_block(const uint32_t* keys, const int32_t
 __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const PageSelectParams P) {
   extern __shared__ __align__(16) uint8_t s_buf[];
   __shared__ float s_qscale[kSelHeads];
-  __shared__ float s_best[kSelHeads / 16][kSelTile];  // [16 heads][page]
+  __shared__ float s_best[kSelHeads / 32][kSelTile];  // [32 heads][page]
+  __shared__ uint64_t s_done;                         // the tile's products
+  __shared__ uint32_t s_tmem;
   __shared__ int s_hist[256];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
@@ -481,13 +481,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
     }
   };
   const int row0 = rank + nrank * warp, row_step = nrank * (kSelThreads / 32);
-  const int page_of_thread = tid >> 3;  // of a tile: eight threads load a page's key
+  const int tile = P.tile;
+  const int key_shift = tile == kSelTile ? 2 : 3;  // 4 or 8 threads load a page's key
+  const int page_of_thread = tid >> key_shift;
   uint4 raw[3];
   int entry = 0;  // the table's entry of the first tile's page
   if (P.topk > 1 && P.topk < P.max_pages) {
     if (row0 < min(kSelHeads, P.h_q)) load_row(row0, raw);
-    if (rank * kSelTile + page_of_thread < P.max_pages)
-      entry = table[rank * kSelTile + page_of_thread];
+    if (rank * tile + page_of_thread < P.max_pages) entry = table[rank * tile + page_of_thread];
   }
   const int seen = tokens_seen(P, pair);
   const int last = (seen + kPage - 1) / kPage - 1;  // -1: the query sees nothing
@@ -495,25 +496,39 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
 
   if (choose) {
     cluster_arrive();  // this CTA runs: the others may store to its shared memory
-    const int rows = select_rows(P.h_q);
-    uint8_t* s_q = s_buf;
-    uint8_t* s_keys = s_buf + rows * kSelStride;
-    const int tiles = (last + kSelTile - 1) / kSelTile;
+    const int q_rows = select_rows(P.h_q);
+    // (swizzle atoms are 512 bytes; the offset is the same in every CTA)
+    uint8_t* s_keys = s_buf + ((1024 - (ptx::smem_u32(s_buf) & 1023)) & 1023);
+    uint8_t* s_q = s_keys + 2 * kSelKeyBytes;
+    constexpr int kMmaWarp = kSelThreads / 32 - 1;  // the one with the fewest head rows
+    if (warp == kMmaWarp) {
+      if (lane == 0) {
+        ptx::mbar_init(&s_done, 1);
+        ptx::fence_mbar_init();
+      }
+      __syncwarp();
+      ptx::tmem_alloc(&s_tmem, kSelTmemCols);
+      ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();  // seen by all threads behind the cluster barrier below
+    int done = 0;            // tiles multiplied
+    const int tiles = (last + tile - 1) / tile;
     // a tile's keys, 36 units of 16 bytes each; blk: the table's entry
     auto load_tile = [&](int t, int buf, int blk) {
-      if (t < tiles && t * kSelTile + page_of_thread < last) {
+      if (t < tiles && t * tile + page_of_thread < last) {
         blk = clamp_block(blk, P.num_blocks);
         const int8_t* src = P.keys + static_cast<size_t>(blk) * kD;
-        const uint32_t dst = ptx::smem_u32(s_keys) + (buf * kSelTile + page_of_thread) * kSelStride;
-        for (int u = tid & 7; u < kD / 16; u += 8)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * u),
+        const uint32_t dst = ptx::smem_u32(s_keys) + buf * kSelKeyBytes;
+        for (int u = tid & ((1 << key_shift) - 1); u < kSelUnits; u += 1 << key_shift)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           dst + sel_offset(kSelTile, page_of_thread, u)),
                        "l"(src + 16 * u)
                        : "memory");
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto entry_of = [&](int t) {
-      const int p = t * kSelTile + page_of_thread;
+      const int p = t * tile + page_of_thread;
       return t < tiles && p < last ? table[p] : 0;
     };
     for (int h0 = 0; h0 < P.h_q; h0 += kSelHeads) {
@@ -522,8 +537,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
         if (h0 + row0 < P.h_q && row0 < kSelHeads) load_row(h0 + row0, raw);
         cluster_arrive();  // the previous pass is done with the codes
       }
-      load_tile(rank, 0, entry);
-      entry = entry_of(rank + nrank);
+      // the key loads of half of the warps go ahead of their head rows, those of
+      // the others behind their first: the rows' shuffles and stores wait in line
+      // behind loads
+      const bool keys_first = warp >= kSelThreads / 64;
+      if (keys_first) load_tile(rank, 0, entry);
       bool stored = false;
       const int nh = min(kSelHeads, P.h_q - h0);
       for (int r = row0; r < nh; r += row_step) {
@@ -561,98 +579,93 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
           cluster_wait();
           stored = true;
         }
-        const uint32_t dst = ptx::smem_u32(s_q) + r * kSelStride;
+        const uint32_t dst = ptx::smem_u32(s_q);
         for (int c = 0; c < nrank; ++c) {
           const uint32_t to = ptx::mapa_shared(dst, c);
 #pragma unroll
           for (int j = 0; j < 3; ++j)
-            if (lane + 32 * j < kD / 8) st_cluster_v2(to + 8 * (lane + 32 * j), code[j].x, code[j].y);
+            if (const int v = lane + 32 * j; v < kD / 8)  // half a unit
+              st_cluster_v2(to + sel_offset(q_rows, r, v >> 1) + 8 * (v & 1), code[j].x, code[j].y);
           if (lane == 0) st_cluster(ptx::mapa_shared(ptx::smem_u32(&s_qscale[r]), c), scale);
         }
+        if (!keys_first && r == row0) load_tile(rank, 0, entry);
       }
       if (!stored) cluster_wait();
+      if (!keys_first && row0 >= nh) load_tile(rank, 0, entry);
+      entry = entry_of(rank + nrank);
       cluster_arrive();  // this warp's codes are stored
       cluster_wait();
 
-      // 16 heads a warp, and 16 pages of a tile, or 32 where more than 64 heads
-      // leave only two warps to 16 heads
-      const bool wide = nh > 64;
-      const int hg = wide ? warp >> 1 : warp >> 2;
-      const int page0 = wide ? 32 * (warp & 1) : 16 * (warp & 3);
-      const bool active = 16 * hg < nh;
+      ptx::tc_fence_after();
+      const uint32_t tmem = s_tmem;
+      const int n16 = (nh + 15) / 16 * 16;  // rows past nh: whatever lies there, not looked at
       const bool final_pass = h0 + kSelHeads >= P.h_q;
       // the table's entry of the page whose score this thread finishes next
       int scale_entry = 0;
-      if (tid < kSelTile && rank * kSelTile + tid < last) scale_entry = table[rank * kSelTile + tid];
-      uint32_t a[kD / 32][4];  // A tiles: 16 heads x 32 bytes
-      float unit[2] = {0.f, 0.f};
-      if (active) {
-        const uint32_t a0 = ptx::smem_u32(s_q) + (16 * hg + (lane & 15)) * kSelStride +
-                            16 * (lane >> 4);
-#pragma unroll
-        for (int k = 0; k < kD / 32; ++k) ldmatrix_x4(a[k], a0 + 32 * k);
-#pragma unroll
-        for (int hi = 0; hi < 2; ++hi) unit[hi] = s_qscale[16 * hg + 8 * hi + (lane >> 2)];
-      }
+      if (tid < tile && rank * tile + tid < last) scale_entry = table[rank * tile + tid];
       for (int t = rank, i = 0; t < tiles; t += nrank, ++i) {
         load_tile(t + nrank, (i + 1) & 1, entry);
         entry = entry_of(t + 2 * nrank);
-        const int p = t * kSelTile + tid;
+        const int p = t * tile + tid;
         float key_scale = 0.f, prev = -INFINITY;
-        if (tid < kSelTile && p < last) {
+        if (tid < tile && p < last) {
           key_scale = P.scales[clamp_block(scale_entry, P.num_blocks)];
           if (h0 > 0) prev = __uint_as_float(scores[p]);
         }
-        const int pn = p + nrank * kSelTile;
-        if (tid < kSelTile && pn < last) scale_entry = table[pn];
+        const int pn = p + nrank * tile;
+        if (tid < tile && pn < last) scale_entry = table[pn];
         asm volatile("cp.async.wait_group 1;" ::: "memory");
+        ptx::fence_proxy_async_smem();
         __syncthreads();  // the tile's keys are in shared memory
-        if (active) {
-          int acc[4][4];  // 16 heads x 8 pages each
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0;
-          // B tiles (16 pages x 32 bytes)
-          const uint32_t b0 = ptx::smem_u32(s_keys) +
-                              ((i & 1) * kSelTile + page0 + (lane & 7) + 8 * (lane >> 4)) *
-                                  kSelStride +
-                              16 * ((lane >> 3) & 1);
-#pragma unroll
-          for (int k = 0; k < kD / 32; ++k) {
-            uint32_t b[4];
-            ldmatrix_x4(b, b0 + 32 * k);
-            mma_s8(acc[0], a[k], b[0], b[1]);
-            mma_s8(acc[1], a[k], b[2], b[3]);
-            if (wide) {
-              ldmatrix_x4(b, b0 + 16 * kSelStride + 32 * k);
-              mma_s8(acc[2], a[k], b[0], b[1]);
-              mma_s8(acc[3], a[k], b[2], b[3]);
+        if (warp == kMmaWarp) {
+          ptx::tc_fence_after();
+          if (ptx::elect_one_sync()) {
+            // eight rows are 512 bytes; two steps of 32 bytes a chunk
+            const uint64_t da = ptx::smem_desc(ptx::smem_u32(s_keys) + (i & 1) * kSelKeyBytes, 16,
+                                               8 * kSelChunk, ptx::kLayoutSW64);
+            const uint64_t db =
+                ptx::smem_desc(ptx::smem_u32(s_q), 16, 8 * kSelChunk, ptx::kLayoutSW64);
+            const uint32_t idesc = ptx::idesc_s8_s32(kSelTile, n16);
+#pragma unroll 1
+            for (int k = 0; k < kD / 32; ++k) {
+              const int in = 2 * (k & 1), c = k >> 1;  // 32 bytes within chunk c
+              ptx::umma_i8_ss(tmem, da + c * (kSelTile * kSelChunk / 16) + in,
+                              db + c * (q_rows * kSelChunk / 16) + in, idesc, k ? 1u : 0u);
             }
+            ptx::umma_commit(&s_done);
           }
-          // max over the 16 heads of s_h * dot, per page
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            if (n >= 2 && !wide) break;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float v = -INFINITY;
-#pragma unroll
-              for (int hi = 0; hi < 2; ++hi)
-                if (16 * hg + 8 * hi + (lane >> 2) < nh)
-                  v = fmaxf(v, static_cast<float>(acc[n][2 * hi + e]) * unit[hi]);
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-              if (lane < 4) s_best[hg][page0 + 8 * n + 2 * lane + e] = v;
-            }
-          }
+          __syncwarp();
         }
+        // (a wait that runs out is on record; the scores are then worthless)
+        ptx::mbar_wait(&s_done, done & 1, 0x79);
+        ++done;
+        ptx::tc_fence_after();
+        // the lane's page, heads 32 hg .. + 31: max of s_h * dot
+        const int hg = warp >> 2, h_first = 32 * hg;
+        if (h_first < nh && 32 * (warp & 3) < tile) {
+          const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + h_first;
+          float d[32];
+          if (h_first + 32 <= n16) {
+            ptx::tmem_ld32(at, d);
+            ptx::tmem_ld_wait_regs(d);
+          } else {
+            ptx::tmem_ld16(at, d);
+            ptx::tmem_ld_wait_regs16(d);
+          }
+          float v = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (h_first + c < nh)
+              v = fmaxf(v, static_cast<float>(__float_as_int(d[c])) * s_qscale[h_first + c]);
+          s_best[hg][32 * (warp & 3) + lane] = v;
+        }
+        ptx::tc_fence_before();
         __syncthreads();  // s_best is complete, the tile's buffer free
-        if (tid < kSelTile && p < last) {
+        if (tid < tile && p < last) {
           float v = prev;
 #pragma unroll
-          for (int g = 0; g < kSelHeads / 16; ++g)
-            if (16 * g < nh) v = fmaxf(v, s_best[g][tid]);
+          for (int g = 0; g < kSelHeads / 32; ++g)
+            if (32 * g < nh) v = fmaxf(v, s_best[g][tid]);
           // + 0: a product that underflows to -0 ties with 0
           scores[p] = final_pass ? max(order_key(v * key_scale + 0.f), 1u) : __float_as_uint(v);
         }
@@ -660,6 +673,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     cluster_arrive();  // this CTA's scores are written
+    if (warp == kMmaWarp) {
+      ptx::tc_fence_after();
+      ptx::tmem_dealloc(s_tmem, kSelTmemCols);
+    }
     cluster_wait();
   }
   if (rank != 0) return;

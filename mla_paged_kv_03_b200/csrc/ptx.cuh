@@ -190,6 +190,17 @@ __device__ __forceinline__ void umma_f16_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// The same for kind::i8 (signed bytes in, int32 accumulators, K = 32).
+__device__ __forceinline__ void umma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on the mbarrier when all previously issued tcgen05 ops of this
 // thread complete.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
@@ -498,6 +509,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes
 }
 
 constexpr uint32_t kLayoutSW128 = 2;
+constexpr uint32_t kLayoutSW64 = 4;
 
 // A descriptor split into its two 32-bit words.  The start address lives in
 // the low 14 bits of `lo`, so stepping an operand by `bytes` inside shared
@@ -528,6 +540,12 @@ __device__ __forceinline__ void umma_f16_ss_w(uint32_t d_tmem, uint32_t a_lo, ui
 
 // Instruction descriptor for kind::f16: bf16 x bf16 -> fp32, M x N, with the
 // major-ness of A and B (0 = K-major, 1 = MN-major).
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {  // both K-major
+  return (2u << 4)                          // D = s32
+         | (1u << 7)                        // A = s8
+         | (1u << 10)                       // B = s8
+         | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {
   return (1u << 4)                          // D = fp32
          | (1u << 7)                        // A = bf16
