@@ -24,14 +24,17 @@
 // and its maximum takes 4, 2 or 1 shuffles.  A warp keeps its gains in registers and
 // strides over the tokens.
 //
-// Precision: the squares of the norm are exact in fp32 and summed there, sixteen
-// a lane in two chains and then over the lanes (about 2^-24 of the sum at most,
-// half of that in 1/sqrt, which is formed in fp64); sums near fp32's limits are
-// formed in fp64.  y has two further roundings, of g / rms and of the product: a
-// code differs from the definition's only where y lies within a few 2^-24 of a
-// rounding border.
+// Precision: the norm's sum of squares and 1/sqrt are formed in fp64, y in fp32
+// with the exact products' low parts carried along (one rounding), quotients with
+// one more; with the rounded maximum and scale that is 2^-22 of a quotient.  One
+// that lies within 2^-21 of a rounding border is decided in fp64 from the latent
+// (rotated dims, whose error is relative to their pair: within 2^-18), so that the
+// codes are those of the definition in fp64, but for rotated dims that cancel to
+// less than a 16th of their pair.  (32768 tokens into FP4 rows: 29 us; 24 us
+// without the second look, where a few codes in a million differ, and 21 us with
+// the squares in fp32 and y = x (g / rms), where some ten do.)
 //
-// Bound: bulk calls by instructions (some 400 a token and warp; the quotients by
+// Bound: bulk calls by instructions (some 550 a token and warp; the quotients by
 // one multiplication and one correction each, not by division), steps of a few
 // tokens by one chain of latencies, so the slot, the position and the row are
 // read side by side.
@@ -45,8 +48,8 @@
 namespace mla {
 
 constexpr int kRow1152 = 2 * kD;  // bf16 cache row
-constexpr int kAppendWarps = 8;
-constexpr int kAppendCtas = 5;  // CTAs per SM of a full grid
+constexpr int kAppendWarps = 4;
+constexpr int kAppendCtas = 6;  // CTAs per SM of a full grid
 
 struct AppendParams {
   const __nv_bfloat16* kv;  // [n] rows of d values, kv_stride values apart
@@ -62,6 +65,14 @@ struct AppendParams {
   __nv_bfloat16* rows;  // [n, d], or null
 };
 
+// x * g * inv with one rounding, inv = inv_hi + inv_lo: the product x g is held
+// exactly as hi + lo, and the small products join hi * inv_hi inside the last fma.
+__device__ __forceinline__ float mul3_once(float x, float g, float inv_hi, float inv_lo) {
+  const float hi = x * g;
+  const float lo = fmaf(x, g, -hi);
+  return fmaf(hi, inv_hi, fmaf(lo, inv_hi, hi * inv_lo));
+}
+
 // 1/sqrt(v) for v in fp32's normal range: the fp32 value (2^-22) and one Newton
 // step in fp64 (3/8 of its error squared: below 2^-44).
 __device__ __forceinline__ double inv_root(double v) {
@@ -69,20 +80,8 @@ __device__ __forceinline__ double inv_root(double v) {
   return fma(0.5 * r, fma(-v * r, r, 1.0), r);
 }
 
-// 1/sqrt(mean square + eps) of a row whose sum of squares leaves the range of
-// fp32, from its raw 16-byte units; every lane of the warp calls it.
-__device__ __noinline__ double inv_root_by_fp64(uint4 a, uint4 b, double eps) {
-  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  double ss = 0.0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const double lo = __uint_as_float(u[e] << 16), hi = __uint_as_float(u[e] & 0xFFFF0000u);
-    ss = fma(lo, lo, fma(hi, hi, ss));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  return 1.0 / sqrt(ss * (1.0 / kNope) + eps);
-}
+// The same outside of it, kept out of line.
+__device__ __noinline__ double inv_root_far(double v) { return 1.0 / sqrt(v); }
 
 // y / scale for eight values.  kSmall: the scale may leave the range in which
 // its reciprocal serves.
@@ -117,6 +116,17 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float* v, uint32_t (&h)[4])
   return w;
 }
 
+// E2M1 code pair (low nibble first) -> two fp32 values (exact).
+__device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b0, b1;\n\t"
+      "mov.b16 {b0, b1}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+      : "=r"(h)
+      : "h"(static_cast<uint16_t>(byte)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // E4M3 code pair -> two fp32 values (exact).
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t pair) {
   uint32_t h;
@@ -148,6 +158,81 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4 w, float* x) {
     x[2 * e] = __uint_as_float(u[e] << 16);
     x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
   }
+}
+
+// fp64 -> fp32 rounded to odd: rounding that to nearest in a shorter format gives
+// the correctly rounded value of v.
+__device__ __forceinline__ float round_odd(double v) {
+  const float f = __double2float_rz(v);
+  return static_cast<double>(f) != v ? __uint_as_float(__float_as_uint(f) | 1u) : f;
+}
+
+// A lane's unit (8 dims) formed in fp64 from the latent.  gain: of the unit, or
+// null; rotated: lanes 24.. hold units to rotate, lane l the `turns` of pair l.
+// Every lane of the warp calls it.
+__device__ __forceinline__ void unit_by_fp64(uint4 raw, const float* gain, double inv, bool rotated,
+                                             int position, double turns, double (&y)[8]) {
+  const int lane = threadIdx.x & 31;
+  float x[8];
+  unpack_bf16x8(raw, x);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = gain ? static_cast<double>(x[k]) * gain[k] * inv : x[k];
+  if (!rotated) return;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const double a = position * __shfl_sync(0xffffffffu, turns, (4 * (lane - 24) + k) & 31);
+    double s, c;
+    sincospi(2.0 * (a - rint(a)), &s, &c);
+    if (lane < 24) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // (indexes known to the compiler)
+      if (e == k) {
+        const double p = y[2 * e], q = y[2 * e + 1];
+        y[2 * e] = p * c - q * s;
+        y[2 * e + 1] = p * s + q * c;
+      }
+  }
+}
+
+// Its group's maximum magnitude.
+template <int kGroupLanes>
+__device__ __forceinline__ double amax_by_fp64(const double (&y)[8]) {
+  double amax = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) amax = fmax(amax, fabs(y[k]));
+#pragma unroll
+  for (int o = kGroupLanes / 2; o > 0; o >>= 1)
+    amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  return amax;
+}
+
+// Rarely called, by a whole warp, and kept out of line: a unit's codes as fp64 has them (E4M3 in .x
+// and .y, or E2M1 in .x; scale: as stored, the 656-byte rows take the group's own
+// absmax/448, unrounded), and the E4M3 code of absmax/6.
+template <int kRowBytes>
+__device__ __noinline__ uint2 codes_by_fp64(uint4 raw, const float* gain, double inv, bool rotated,
+                                            int position, double turns, float scale) {
+  double y[8], unit = scale;
+  unit_by_fp64(raw, gain, inv, rotated, position, turns, y);
+  if constexpr (kRowBytes == kRow656) {
+    const double amax = amax_by_fp64<16>(y);
+    if (amax > 0.0) unit = amax / 448.0;
+  }
+  float c[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) c[k] = round_odd(y[k] / unit);
+  if constexpr (kRowBytes == kRow288) {
+    uint32_t h[4];
+    return make_uint2(cvt_e2m1x8(c, h), 0u);
+  } else {
+    return make_uint2(cvt_e4m3x4(c[0], c[1], c[2], c[3]), cvt_e4m3x4(c[4], c[5], c[6], c[7]));
+  }
+}
+__device__ __noinline__ uint32_t scale_by_fp64(uint4 raw, const float* gain, double inv,
+                                               bool rotated, int position, double turns) {
+  double y[8];
+  unit_by_fp64(raw, gain, inv, rotated, position, turns, y);
+  return cvt_e4m3x4(round_odd(amax_by_fp64<2>(y) / 6.0), 0.f, 0.f, 0.f) & 0xFFu;
 }
 
 // Rotates the unit's four pairs 4u .. 4u + 3; lane k holds pair k's cos, sin.
@@ -209,30 +294,32 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
     for (int j = 0; j < 2; ++j) unpack_bf16x8(raw[j], y[j]);
     unpack_bf16x8(raw[2], yr);
 
+    double inv = 1.0;
     if (P.gain) {
-      float s0 = 0.f, s1 = 0.f;  // the squares are exact in fp32
+      double s0 = 0.0, s1 = 0.0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s0 = fmaf(y[0][e], y[0][e], s0);
-        s1 = fmaf(y[1][e], y[1][e], s1);
+      for (int e = 0; e < 8; ++e) {  // the squares are exact in fp64
+        const double a = static_cast<double>(y[0][e]), b = static_cast<double>(y[1][e]);
+        s0 = fma(a, a, s0);
+        s1 = fma(b, b, s1);
       }
-      float s = s0 + s1;
+      double ss = s0 + s1;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const double inv = s > 0x1p-80f && s < 0x1p+100f
-                             ? inv_root(static_cast<double>(s) * (1.0 / kNope) + P.eps)
-                             : inv_root_by_fp64(raw[0], raw[1], P.eps);
-      const float inv32 = static_cast<float>(inv);
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const double v = ss * (1.0 / kNope) + P.eps;
+      inv = v > 0x1p-100 && v < 0x1p+100 ? inv_root(v) : inv_root_far(v);
+      const float inv_hi = static_cast<float>(inv);
+      const float inv_lo = static_cast<float>(inv - static_cast<double>(inv_hi));
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float4* g = reinterpret_cast<const float4*>(s_gain + (lane + 32 * j) * 8);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float4 f = g[e];
-          y[j][4 * e] *= f.x * inv32;
-          y[j][4 * e + 1] *= f.y * inv32;
-          y[j][4 * e + 2] *= f.z * inv32;
-          y[j][4 * e + 3] *= f.w * inv32;
+          y[j][4 * e] = mul3_once(y[j][4 * e], f.x, inv_hi, inv_lo);
+          y[j][4 * e + 1] = mul3_once(y[j][4 * e + 1], f.y, inv_hi, inv_lo);
+          y[j][4 * e + 2] = mul3_once(y[j][4 * e + 2], f.z, inv_hi, inv_lo);
+          y[j][4 * e + 3] = mul3_once(y[j][4 * e + 3], f.w, inv_hi, inv_lo);
         }
       }
     }
@@ -257,6 +344,12 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
       for (int j = 0; j < 2; ++j) {
         const int u = lane + 32 * j;
         const int group = u / kGroupLanes;
+        // Without norm and rotation y is exact, and so are the codes; otherwise a
+        // quotient within eps of a rounding border is decided in fp64.
+        const bool rotated = !kWide && P.positions && j == 1;
+        const float eps = !P.gain && !rotated ? 0.f : rotated && lane >= 24 ? 0x1p-18f : 0x1p-21f;
+        const float more = 1.f + eps, less = 1.f - eps;
+        const float* gain = P.gain ? s_gain + u * 8 : nullptr;
         float amax = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[j][e]));
@@ -283,15 +376,37 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
           if (lane % kGroupLanes == 0)
             *reinterpret_cast<float*>(row + kNope + 4 * group) = scale;
         } else {
-          uint32_t code = cvt_e4m3x4(div_by(amax, 6.f, 1.f / 6.f), 0.f, 0.f, 0.f) & 0xFFu;
+          const float sixth = div_by(amax, 6.f, 1.f / 6.f);
+          const uint32_t both = cvt_e4m3x4(sixth * more, sixth * less, 0.f, 0.f);
+          uint32_t code = both & 0xFFu;
+          if (__any_sync(0xffffffffu, code != (both >> 8 & 0xFFu)))
+            code = scale_by_fp64(raw[j], gain, inv, rotated, position, turns);
           if (code == 0) code = 0x38;  // 1.0, of a zero or tiny group
           scale = e4m3x2_to_float2(code).x;
           quotients8<false>(y[j], scale, c);
           if (lane % kGroupLanes == 0) row[kNope / 2 + group] = static_cast<uint8_t>(code);
         }
         if constexpr (kRowBytes == kRow288) {
-          uint32_t h[4];
-          const uint32_t w = cvt_e2m1x8(c, h);
+          float up[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            up[k] = c[k] * more;
+            c[k] *= less;
+          }
+          uint32_t h[4], other[4];
+          uint32_t w = cvt_e2m1x8(up, h);
+          const uint32_t near = __ballot_sync(0xffffffffu, w != cvt_e2m1x8(c, other));
+          if (near) {
+            const uint2 exact = codes_by_fp64<kRowBytes>(
+                raw[j], gain, inv, rotated && near >> 24, position, turns, scale);
+            if (near >> lane & 1) w = exact.x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = e2m1x2_to_float2((w >> (8 * k)) & 0xFFu);
+              const __half2 hv = __floats2half2_rn(f.x, f.y);
+              h[k] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+          }
           *reinterpret_cast<uint32_t*>(row + u * 4) = w;
           if (out) {
 #pragma unroll
@@ -303,8 +418,19 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
             *reinterpret_cast<uint4*>(out + u * 8) = scaled_bf16x8<true>(c, scale);
           }
         } else {
-          const uint32_t lo = cvt_e4m3x4(c[0], c[1], c[2], c[3]);
-          const uint32_t hi = cvt_e4m3x4(c[4], c[5], c[6], c[7]);
+          uint32_t lo = cvt_e4m3x4(c[0] * more, c[1] * more, c[2] * more, c[3] * more);
+          uint32_t hi = cvt_e4m3x4(c[4] * more, c[5] * more, c[6] * more, c[7] * more);
+          const uint32_t near = __ballot_sync(
+              0xffffffffu, lo != cvt_e4m3x4(c[0] * less, c[1] * less, c[2] * less, c[3] * less) ||
+                               hi != cvt_e4m3x4(c[4] * less, c[5] * less, c[6] * less, c[7] * less));
+          if (near) {
+            const uint2 exact = codes_by_fp64<kRowBytes>(
+                raw[j], gain, inv, rotated && near >> 24, position, turns, scale);
+            if (near >> lane & 1) {
+              lo = exact.x;
+              hi = exact.y;
+            }
+          }
           *reinterpret_cast<uint2*>(row + u * 8) = make_uint2(lo, hi);
           if (out) {
 #pragma unroll

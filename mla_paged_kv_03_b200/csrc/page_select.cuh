@@ -448,6 +448,11 @@ __device__ __forceinline__ void select_block(const uint32_t* keys, const int32_t
 // The keys are 576 bytes a page, 1/128 of the rows they stand for: latency, not
 // bytes, bounds this step, hence one launch for plan, scores and selection, and
 // the query, the table and the length read side by side at its start.
+// B200, 32 queries x 128 heads over 1024 pages: 75 us as three launches (scores by
+// a CTA per 128 pages, each quantising all heads by division), 20 us as one
+// cluster with mma.sync (its shared-memory reads took as long as its products),
+// 13 us with tcgen05: 5 us until the codes are everywhere, 4 us for the tiles,
+// 3 us for the selection.
 __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const PageSelectParams P) {
   extern __shared__ __align__(16) uint8_t s_buf[];
   __shared__ float s_qscale[kSelHeads];

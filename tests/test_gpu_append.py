@@ -202,6 +202,54 @@ def test_norm_of_rows_whose_squares_leave_fp32(fmt, size, eps):
     run(fmt, 40, values=x.to(torch.bfloat16), eps=eps, seed=10)
 
 
+@pytest.mark.parametrize("fmt", ["656", "528", "288"])
+@pytest.mark.parametrize("rope", [False, True])
+def test_codes_are_those_of_fp64(fmt, rope):
+    """The codes equal the definition's in fp64 (656-byte rows: with the unrounded absmax/448),
+    except for rotated dims that nearly cancel and values within 2^-45 of a border."""
+    n, d, gen = 6000, width(fmt), torch.Generator().manual_seed(31)
+    kv = torch.randn((n, d), generator=gen).to(torch.bfloat16)
+    gain = 1 + 0.1 * torch.randn(512, generator=gen)
+    positions = torch.randint(0, 1 << 17, (n,), generator=gen, dtype=torch.int32)
+    cache = make_cache(fmt, n // 64 + 1, "cuda", gen)
+    B.mla_cache_append(kv.cuda(), torch.arange(n, dtype=torch.int32, device="cuda"), cache,
+                       positions=positions.cuda() if rope else None, norm_gain=gain.cuda())
+    raw = raw_rows(cache)[:n]
+    y, size = expected(kv, positions if rope else None, gain, 1e-6, 1e4)
+    y, size = y[:, :512], size[:, :512]
+    per = {"656": 128, "528": 32, "288": 16}[fmt]
+    g = y.reshape(n, 512 // per, per)
+    amax = g.abs().amax(2, keepdim=True)
+
+    def e4m3_step(v):
+        return torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+
+    def e2m1_step(v):
+        return torch.where(v.abs() < 2, 0.5, torch.where(v.abs() < 4, 1.0, 2.0)).double()
+
+    if fmt == "288":
+        scale = amax / 6
+        scale = torch.round(scale / e4m3_step(scale)) * e4m3_step(scale)
+        assert torch.equal(e4m3(raw[:, 256:]), scale[..., 0])
+        code = torch.stack([raw[:, :256] & 15, raw[:, :256] >> 4], 2).reshape(n, 512).long()
+        got = E2M1[code & 7] * torch.where(code >= 8, -1.0, 1.0)
+        step, most = e2m1_step, 6.0
+    else:
+        scale = amax / 448
+        if fmt == "528":
+            scale = torch.exp2(torch.ceil(torch.log2(scale)))
+            assert torch.equal(torch.exp2(raw[:, 512:].double() - 127), scale[..., 0])
+        got = e4m3(raw[:, :512])
+        step, most = e4m3_step, 448.0
+    v = (g / scale).reshape(n, 512)
+    steps = v / step(v)
+    want = (torch.round(steps) * step(v)).clamp(-most, most)
+    border = (steps - torch.floor(steps) - 0.5).abs() < 2.0 ** -45 * steps.abs()
+    cancels = y.abs() < size / 16  # size: 2 |y|, or |a| + |b| of a rotated pair
+    wrong = (got != want) & ~border & ~cancels
+    assert not wrong.any(), f"{int(wrong.sum())} codes differ"
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_append_strided_rows_padding_and_no_rows_output(fmt):
     run(fmt, 77, stride=width(fmt) + 520, pad=(0, 5, 76), seed=4)
