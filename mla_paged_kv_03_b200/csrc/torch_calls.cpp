@@ -11,11 +11,13 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
+#include <exception>
 #include <limits>
-#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -173,8 +175,9 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, Body body) {
     set_library_error(e.code);
   } catch (const BadArgument& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own (out of memory, ..) as torch raises them
+    std::exception_ptr e = std::current_exception();
+    torch::translate_exception_to_python(e);
   }
   return nullptr;
 }

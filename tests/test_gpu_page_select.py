@@ -406,6 +406,40 @@ def test_slot_trace_names_the_taken_rows():
     c.check(got, 3)
 
 
+def test_wider_indexes_and_strided_inputs():
+    c = Case([900, 333], h_q=16, s_q=2, seed=19)
+    want = c.run(4)
+    q = torch.empty((2, 2, 16, 600), dtype=torch.bfloat16, device="cuda")[..., :576]
+    q.copy_(c.q)
+    table = torch.empty((2, 2 * c.table.shape[1]), dtype=torch.int64, device="cuda")[:, ::2]
+    table.copy_(c.table)
+    keys, scales = c.keys.cuda(), c.scales.cuda()
+    got = B.mla_page_sparse_decode(q, c.cache.cuda(), keys, scales, table, c.sl().long(), 4,
+                                   softmax_scale=c.scale)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    B.mla_page_keys_update(c.cache.cuda(), table, c.sl().long(), keys, scales)
+    owned = c.table[c.table >= 0].long()
+    assert torch.equal(keys.cpu()[owned], c.keys[owned])
+
+
+def test_two_streams_at_once():
+    a, b = Case([64 * 150 + 3] * 3, h_q=128, seed=23), Case([5000, 64], h_q=16, seed=24)
+    ta = (a.q.cuda(), a.cache.cuda(), a.keys.cuda(), a.scales.cuda(), a.table.cuda(), a.sl())
+    tb = (b.q.cuda(), b.cache.cuda(), b.keys.cuda(), b.scales.cuda(), b.table.cuda(), b.sl())
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        with torch.cuda.stream(sa):
+            x = B.mla_page_sparse_decode(*ta, 7, softmax_scale=a.scale)
+        with torch.cuda.stream(sb):
+            y = B.mla_page_sparse_decode(*tb, 3, softmax_scale=b.scale)
+        got.append((x, y))
+    for x, y in got:
+        a.check(x, 7)
+        b.check(y, 3)
+
+
 def test_rejects_wrong_arguments():
     c = Case([500, 450], seed=17)
     good = dict(q=c.q.cuda(), kcache=c.cache.cuda(), page_keys=c.keys.cuda(),

@@ -246,6 +246,16 @@ def test_a_plan_of_another_prefix_length_is_refused_on_the_device():
     c.check(c.run())
 
 
+def test_wider_indexes_and_strided_inputs():
+    c = Case([70, 64, 0], 200, 2, 16, seed=21)
+    want = c.run()
+    q, cache, pt, table, sl = c.dev()
+    wide = torch.empty((3, 2, 16, 640), dtype=torch.bfloat16, device="cuda")[..., :576]
+    wide.copy_(q)
+    got = c.run(t=(wide, cache, pt.long(), table.long().t().contiguous().t(), sl))
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_rejects_outputs_and_workspaces_of_other_shapes():
     c = Case([70, 64], 130, 1, 16, seed=13)
     for bad in (dict(out=torch.empty((2, 1, 15, 512), dtype=torch.bfloat16, device="cuda")),
