@@ -344,10 +344,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
       for (int j = 0; j < 2; ++j) {
         const int u = lane + 32 * j;
         const int group = u / kGroupLanes;
-        // Without norm and rotation y is exact, and so are the codes; otherwise a
-        // quotient within eps of a rounding border is decided in fp64.
+        // Without norm or rotation a dim is exact, and so is its code (and bf16 values
+        // often lie on a border); otherwise a quotient within eps of a rounding border
+        // is decided in fp64.
         const bool rotated = !kWide && P.positions && j == 1;
-        const float eps = !P.gain && !rotated ? 0.f : rotated && lane >= 24 ? 0x1p-18f : 0x1p-21f;
+        const float eps = rotated && lane >= 24 ? 0x1p-18f : P.gain ? 0x1p-21f : 0.f;
         const float more = 1.f + eps, less = 1.f - eps;
         const float* gain = P.gain ? s_gain + u * 8 : nullptr;
         float amax = 0.f;
