@@ -322,10 +322,6 @@ __global__ void __launch_bounds__(Threads<kMode>::value, 1)
   constexpr int NPm = kPSplit ? 1 : kNP;
   static_assert(!kPSplit || kNP >= 2, "the hi/lo P pair needs two P buffer regions");
 
-  ptx::grid_dep_wait();    // the planner's metadata is complete
-  ptx::grid_dep_launch();  // the combine grid may be scheduled as CTAs retire
-  const int32_t* meta = P.metadata + part * kMetaInts;
-  if (meta[0] > meta[2]) return;  // empty part: nothing to do (uniform exit)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNPair; ++i) {
@@ -360,12 +356,19 @@ __global__ void __launch_bounds__(Threads<kMode>::value, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = C.tmem_base;
 
+  // (the setup above ran while the planner, or what else came before, still did)
+  ptx::grid_dep_wait();    // the planner's metadata is complete
+  ptx::grid_dep_launch();  // the combine grid may be scheduled as CTAs retire
+  const int32_t* meta = P.metadata + part * kMetaInts;
+  const bool empty = meta[0] > meta[2];  // nothing to do
   UnitIter it;
   it.init(meta);
 
   constexpr int kL = Loaders<kMode>::value;
   constexpr int kFirstExtraLoader = 2 + 4 * kSoftmaxGroups;
-  if (warp == 0 || warp >= kFirstExtraLoader) {
+  if (empty) {
+    // on to the teardown
+  } else if (warp == 0 || warp >= kFirstExtraLoader) {
     // ============================== loaders ==============================
     // Pair slot j of the ring is filled by loader warp j % kL (whole warp,
     // one elected lane issues the copies).  Warp 0 also loads Q.

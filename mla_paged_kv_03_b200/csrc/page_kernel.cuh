@@ -111,10 +111,6 @@ __global__ void __launch_bounds__(PageCfg::kThreads, 1)
   const int part = blockIdx.x / P.n_groups;
   const int grp = blockIdx.x % P.n_groups;
 
-  ptx::grid_dep_wait();    // the planner's metadata is complete
-  ptx::grid_dep_launch();  // the combine grid may be scheduled as CTAs retire
-  const int32_t* meta = P.metadata + part * kMetaInts;
-  if (meta[0] > meta[2]) return;  // empty part
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNPair; ++i) {
@@ -154,6 +150,11 @@ __global__ void __launch_bounds__(PageCfg::kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = C.tmem_base;
 
+  // (the setup above ran while the planner, or what else came before, still did)
+  ptx::grid_dep_wait();    // the planner's metadata is complete
+  ptx::grid_dep_launch();  // the combine grid may be scheduled as CTAs retire
+  const int32_t* meta = P.metadata + part * kMetaInts;
+  const bool empty = meta[0] > meta[2];  // nothing to do
   UnitIter it;
   it.init(meta);
   // Pages [2 lo, min(2 hi, pages of the sequence)) of a unit; none for L = 0.
@@ -167,7 +168,9 @@ __global__ void __launch_bounds__(PageCfg::kThreads, 1)
     return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, site));
   };
 
-  if (warp == 0 || warp == 2 + Cfg::kSmWarps) {
+  if (empty) {
+    // on to the teardown
+  } else if (warp == 0 || warp == 2 + Cfg::kSmWarps) {
     // ============================== loaders ==============================
     // Load items in order: per page its four pair slots, then its rope slot;
     // item i is issued by loader (i % 2), which waits for the slot first.

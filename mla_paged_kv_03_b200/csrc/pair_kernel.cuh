@@ -146,13 +146,16 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
   const int grp = pair % P.n_groups;  // 128-row group
 
   const int nqk = P.qk_chunks ? P.qk_chunks : kNumChunks;  // 64-dim chunks of q . k
-  ptx::grid_dep_wait();    // the planner's metadata is complete
-  ptx::grid_dep_launch();  // the combine grid may be scheduled as CTAs retire
   const int32_t* meta = P.metadata + part * kMetaInts;
-  if (meta[0] > meta[2]) return;  // empty part: both CTAs of the pair leave together
   constexpr Mode kUnits = kShared ? kSharedPrefix : kDense;
   if constexpr (kShared) {
-    // a plan made for other units names none of these: leave (both CTAs alike)
+    // (Here the wait for what came before stays ahead of the setup: the kernel
+    // follows no planner of its own call, and with the wait behind it the
+    // compiler's code took 3 to 12% longer.)
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();  // the merge grid may be scheduled as CTAs retire
+    if (meta[0] > meta[2]) return;  // empty part: both CTAs of the pair leave together
+    // a plan made for other units or another prefix names none of these
     if (meta[5] != P.batch || meta[6] != P.prefix_len) {
       if (threadIdx.x == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x47);
       return;
@@ -194,6 +197,13 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
   // leader-side barrier addresses in the shared::cluster window
   auto leader_addr = [&](uint64_t* bar) { return ptx::mapa_shared(ptx::smem_u32(bar), 0); };
 
+  bool empty = false;
+  if constexpr (!kShared) {
+    // the setup above ran while the planner, or what else came before, still did
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    empty = meta[0] > meta[2];  // nothing to do, for both CTAs of the pair
+  }
   UnitIter it;
   it.init(meta);
 
@@ -240,7 +250,9 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
     }
   };
 
-  if (warp == 0 || warp >= 2 + kSoftmaxWarps) {
+  if (empty) {
+    // on to the teardown
+  } else if (warp == 0 || warp >= 2 + kSoftmaxWarps) {
     // ======================= loaders (both CTAs); warp 0 also loads Q =======================
     const int role = warp == 0 ? 0 : warp - (1 + kSoftmaxWarps);  // 0 .. kLoaders - 1
     uint32_t st_it = 0;  // stage loads so far (every loader counts all of them)
