@@ -314,9 +314,10 @@ MLA_API int mla_sparse_fused_norm_rope_attn_rope_cast(
  *   metadata, num_splits, num_sm_parts: from mla_shared_prefix_get_metadata
  *                 for the same cache_seqlens, rows_per_kv = s_q * h_q and
  *                 prefix_len; num_sm_parts from mla_num_sm_parts(device, 128,
- *                 1).  Sizes from mla_shared_prefix_metadata_size.  A plan of
- *                 other row groups or another prefix_len is not run: it sets
- *                 the bad-index status and leaves out and lse as they were
+ *                 1).  Sizes from mla_shared_prefix_metadata_size.  A plan
+ *                 made for another batch, rows_per_kv, prefix_len or
+ *                 num_sm_parts is not run: it sets the bad-index status and
+ *                 leaves out and lse as they were
  *   workspace     >= mla_shared_prefix_workspace_size() bytes, 16-byte aligned
  * At most 8192 groups of 128 query rows (over the prefix plus over own
  * tokens).  Other arguments, ownership and errors as in mla_decode_fwd; a

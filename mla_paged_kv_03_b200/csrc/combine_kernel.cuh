@@ -353,13 +353,12 @@ __global__ void __launch_bounds__(kPlanThreads) mla_plan_kernel(const int32_t* s
 }
 
 // Units of a shared-prefix decode: n_prefix of prefix_len tokens, then
-// own_groups for each sequence's own tokens.  Entries 5 and 6 of each metadata
-// row hold the unit count and the prefix length, by which the decode recognises
-// its plan.
+// own_groups for each sequence's own tokens.  Entries 5 to 7 of each metadata
+// row say what the plan is for (shared_plan_key).
 __global__ void __launch_bounds__(kPlanThreads)
     mla_shared_plan_kernel(const int32_t* seqlens, int units, int n_prefix, int prefix_len,
-                           int own_groups, int num_parts, const PlanParams pp, int32_t* metadata,
-                           int32_t* num_splits) {
+                           int own_groups, int rows_per_kv, int num_parts, const PlanParams pp,
+                           int32_t* metadata, int32_t* num_splits) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   __shared__ int32_t C[kPlanMaxBatch + 1];
@@ -368,16 +367,17 @@ __global__ void __launch_bounds__(kPlanThreads)
       units, num_parts, pp, C, metadata, num_splits, nullptr, nullptr, 0);
   __syncthreads();
   for (int p = threadIdx.x; p < num_parts; p += kPlanThreads) {
-    metadata[p * kMetaInts + 5] = units;
+    metadata[p * kMetaInts + 5] = shared_plan_key(units, num_parts);
     metadata[p * kMetaInts + 6] = prefix_len;
+    metadata[p * kMetaInts + 7] = rows_per_kv;
   }
 }
 
 // Merge of a shared-prefix decode: a query row's partials are those of its
 // prefix unit and those of its sequence's own-token unit.
 struct SharedCombineParams {
-  int units, prefix_len, n_prefix, own_groups, R, total_rows;
-  const int32_t* metadata;    // entries 5 and 6: the plan's unit count and prefix length
+  int plan_key, prefix_len, n_prefix, own_groups, R, total_rows;
+  const int32_t* metadata;    // entries 5 to 7: what the plan is for
   const int32_t* num_splits;  // [units + 1]
   const float* ws_o;          // [splits, 128, 512]
   const float* ws_lse;        // [splits, 128]
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   __shared__ float4 s_acc[kRowPerCta ? kCombineWarps - 1 : 1][kNope / 4];
   ptx::grid_dep_wait();  // the attention kernel's partials are complete
   // not this decode's plan: the attention kernel said so
-  if (P.metadata[5] != P.units || P.metadata[6] != P.prefix_len) return;
+  if (P.metadata[5] != P.plan_key || P.metadata[6] != P.prefix_len || P.metadata[7] != P.R) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = kRowPerCta ? blockIdx.x : blockIdx.x * kCombineWarps + warp;
   if (row >= P.total_rows) return;

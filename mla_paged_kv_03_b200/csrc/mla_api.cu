@@ -1186,7 +1186,7 @@ int mla_shared_prefix_get_metadata(const int32_t* cache_seqlens, int batch, int 
   MLA_CHECK_ARG(aligned(cache_seqlens, 4) && aligned(metadata, 4) && aligned(num_splits, 4),
                 "int32 arrays must be 4-byte aligned");
   mla::mla_shared_plan_kernel<<<1, mla::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      cache_seqlens, su.units, su.n_prefix, prefix_len, su.own_groups, num_sm_parts,
+      cache_seqlens, su.units, su.n_prefix, prefix_len, su.own_groups, rows_per_kv, num_sm_parts,
       mla::plan_params_shared(rows_per_kv), metadata, num_splits);
   MLA_CUDA(cudaGetLastError());
   return MLA_OK;
@@ -1263,7 +1263,7 @@ int mla_shared_prefix_decode_fwd(const void* q, const void* kcache, int num_bloc
   if ((rc = launch_pair_decode<false, true>(q, kcache, tkv, p, st)) != MLA_OK) return rc;
 
   mla::SharedCombineParams c{};
-  c.units = su.units;
+  c.plan_key = mla::shared_plan_key(su.units, num_sm_parts);
   c.prefix_len = prefix_len;
   c.n_prefix = su.n_prefix;
   c.own_groups = su.own_groups;

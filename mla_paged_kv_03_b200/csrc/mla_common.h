@@ -78,6 +78,11 @@ MLA_HD inline PlanParams plan_params_shared(int rows_per_kv) {
   return {rows_per_kv > 32 ? kPlanOverheadShared : kPlanOverheadSharedFewRows, 2, 0};
 }
 
+// By entries 5 (this), 6 (prefix length) and 7 (rows per KV head) of each metadata
+// row a shared-prefix decode recognises its plan; units, rows and prefix length
+// fix the batch.  units <= 8192, num_parts <= 1024.
+MLA_HD inline int shared_plan_key(int units, int num_parts) { return units | num_parts << 16; }
+
 // Metadata row per SM part: {begin_b, begin_tile, end_b, end_tile,
 // first_split, 0, 0, 0}; end_tile is exclusive within batch end_b (it may pass
 // that sequence's last tile, see the planner below).

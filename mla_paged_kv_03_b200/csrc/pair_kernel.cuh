@@ -155,8 +155,9 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();  // the merge grid may be scheduled as CTAs retire
     if (meta[0] > meta[2]) return;  // empty part: both CTAs of the pair leave together
-    // a plan made for other units or another prefix names none of these
-    if (meta[5] != P.batch || meta[6] != P.prefix_len) {
+    // a plan made for another call's shapes or parts names none of these units
+    if (meta[5] != shared_plan_key(P.batch, P.num_parts) || meta[6] != P.prefix_len ||
+        meta[7] != P.R) {
       if (threadIdx.x == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x47);
       return;
     }

@@ -246,6 +246,34 @@ def test_a_plan_of_another_prefix_length_is_refused_on_the_device():
     c.check(c.run())
 
 
+def assert_refused(c, plan):
+    q, cache, pt, table, sl = c.dev()
+    out = torch.full((*c.q.shape[:3], 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(c.q.shape[:3], 3.0, device="cuda")
+    B.mla_shared_prefix_decode_fwd(q, cache, pt, c.prefix_len, table, sl, *plan, out=out, lse=lse)
+    assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+    assert (out == 3.0).all() and (lse == 3.0).all()
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("prefix_len", [0, 130])
+def test_a_plan_of_other_rows_with_as_many_units_is_refused(prefix_len):
+    # 2 x 256 rows and 4 x 128 rows: as many units over the prefix, and as many own ones
+    c = Case([70, 64, 300, 0], prefix_len, 1, 128, seed=14)
+    two = torch.tensor([70, 64], dtype=torch.int32, device="cuda")
+    assert_refused(c, B.mla_shared_prefix_get_metadata(two, prefix_len, 256))
+    c = Case([70, 64], prefix_len, 2, 128, seed=15)
+    four = torch.tensor([70, 64, 300, 0], dtype=torch.int32, device="cuda")
+    assert_refused(c, B.mla_shared_prefix_get_metadata(four, prefix_len, 128))
+
+
+@pytest.mark.parametrize("made,used", [(74, 7), (9, 4), (200, 199)])
+def test_a_plan_of_other_parts_is_refused(made, used):
+    c = Case([700, 64, 1000], 1500, 1, 16, seed=16)
+    meta, ns, _ = B.mla_shared_prefix_get_metadata(c.dev()[4], 1500, 16, num_sm_parts=made)
+    assert_refused(c, (meta, ns, used))
+
+
 def test_wider_indexes_and_strided_inputs():
     c = Case([70, 64, 0], 200, 2, 16, seed=21)
     want = c.run()
