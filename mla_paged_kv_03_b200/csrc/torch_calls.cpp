@@ -381,7 +381,7 @@ PyObject* shared_prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     const int b = static_cast<int>(q.size(0)), s_q = static_cast<int>(q.size(1)),
               h_q = static_cast<int>(q.size(2));
     const int parts = whole32(a[8]);
-    const at::Tensor& metadata = tensor(a[6], "metadata");
+    at::Tensor metadata = tensor(a[6], "metadata");
     const at::Tensor& splits = tensor(a[7], "num_splits");
     require(metadata.is_cuda() && splits.is_cuda() && metadata.get_device() == index &&
                 splits.get_device() == index && metadata.scalar_type() == at::kInt &&
@@ -390,10 +390,14 @@ PyObject* shared_prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n_args)
             "metadata and num_splits", "the plan,", index);
     const int rows = static_cast<int>(
         std::min<int64_t>(int64_t{s_q} * h_q, std::numeric_limits<int>::max()));
-    // (a plan of other units is recognised on the device by its metadata)
-    require(parts <= 0 || metadata.numel() >= int64_t{8} * parts,
-            "metadata is too small for num_sm_parts");
-    size_t bytes = 0;
+    // (a plan of another call is recognised on the device by its metadata)
+    size_t bytes = 0, metadata_bytes = 0, splits_bytes = 0;
+    check(mla_shared_prefix_metadata_size(b, rows, prefix_len, parts, &metadata_bytes,
+                                          &splits_bytes));
+    require(metadata.nbytes() >= metadata_bytes, "metadata is too small for num_sm_parts");
+    // num_splits too short for this call is another plan's, whatever the metadata says:
+    // with metadata that names no plan the device refuses it without reading it
+    if (splits.nbytes() < splits_bytes) metadata = at::zeros_like(metadata);
     check(mla_shared_prefix_workspace_size(b, rows, prefix_len, parts, &bytes));
     const at::Device dev = q.device();
     const at::Tensor out = output(a[11], "out", {b, s_q, h_q, kNope}, at::kBFloat16, dev);

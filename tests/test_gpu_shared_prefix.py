@@ -274,6 +274,15 @@ def test_a_plan_of_other_parts_is_refused(made, used):
     assert_refused(c, (meta, ns, used))
 
 
+def test_a_short_num_splits_is_refused():
+    # num_splits of a smaller batch beside matching metadata
+    c = Case([70, 64, 300], 130, 1, 16, seed=17)
+    meta, ns, n = B.mla_shared_prefix_get_metadata(c.dev()[4], 130, 16)
+    assert ns.numel() == 1 + 3 + 1
+    assert_refused(c, (meta, ns[:-1], n))
+    assert_refused(c, (meta, ns[:1].clone(), n))
+
+
 def test_wider_indexes_and_strided_inputs():
     c = Case([70, 64, 0], 200, 2, 16, seed=21)
     want = c.run()
