@@ -356,6 +356,8 @@ MLA_API int mla_shared_prefix_decode_fwd(const void* q, const void* kcache, int 
  *                 mla_decode_fwd, the lengths after the append
  *   page_keys     int8[num_blocks][576], 16-byte aligned; page_scales
  *                 fp32[num_blocks]; only the named pages' entries are written
+ *                 (a block id out of range names none and sets the bad-index
+ *                 status)
  * One launch on `stream`.  batch <= 65535. */
 MLA_API int mla_page_keys_update(const void* kcache, int num_blocks, const int32_t* block_table,
                                  int max_pages, const int32_t* cache_seqlens, int batch,

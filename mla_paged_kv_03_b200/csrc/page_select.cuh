@@ -141,9 +141,13 @@ __global__ void __launch_bounds__(kKeyThreads, 1) mla_page_keys_kernel(const Pag
         const int page = (L + kPage - 1) / kPage - P.tail +
                          static_cast<int>(item - static_cast<long long>(b) * P.tail);
         if (L <= 0 || page < 0) continue;
+        const int entry = P.block_table[static_cast<size_t>(b) * P.max_pages + page];
+        if (entry < 0 || entry >= P.num_blocks) {  // no block: no key to write
+          ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x7a);
+          continue;
+        }
+        blk = entry;
         rows = min(kPage, L - page * kPage);
-        blk = clamp_block(P.block_table[static_cast<size_t>(b) * P.max_pages + page],
-                          P.num_blocks);
       }
       const int g = k % kKeyGroups, round = k / kKeyGroups;
       // the group is done with its last page (and so are the copies of it)

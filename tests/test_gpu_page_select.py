@@ -200,6 +200,32 @@ def test_key_update_reports_bad_inputs_and_stays_in_bounds():
         assert torch.equal(keys[blk].cpu(), code) and torch.equal(scales[blk].cpu(), scale)
 
 
+def test_key_update_writes_no_key_for_a_bad_block():
+    # a bad id must not touch the key of block 0, which another sequence's full page owns
+    c = Case([64 * 3, 64 * 2 + 5], seed=6)
+    c.table[c.table == 0] = int(c.table[0, 0])
+    c.table[0, 0] = 0
+    for b, n in enumerate(c.lengths):
+        for p in range(-(-n // 64)):
+            blk = int(c.table[b, p])
+            c.keys[blk], c.scales[blk] = want_key(c.cache[blk, :min(64, n - 64 * p), 0])
+    named = torch.zeros(c.blocks, dtype=torch.bool)
+    for bad in (-1, c.blocks, -2 ** 31, 2 ** 31 - 1):
+        c.table[1, 2] = bad  # the page of five rows
+        keys = torch.full((c.blocks, 576), 99, dtype=torch.int8, device="cuda")
+        scales = torch.full((c.blocks,), -3.0, device="cuda")
+        update(c, keys, scales)
+        assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+        named[:] = False
+        named[torch.cat([c.table[0], c.table[1, :2]]).long()] = True
+        assert torch.equal(keys.cpu()[named], c.keys[named])
+        assert torch.equal(scales.cpu()[named], c.scales[named])
+        assert (keys.cpu()[~named] == 99).all() and (scales.cpu()[~named] == -3.0).all()
+        update(c, keys, scales, tail=1)
+        assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+        assert torch.equal(keys.cpu()[0], c.keys[0]) and torch.equal(scales.cpu()[0], c.scales[0])
+
+
 # ------------------------------------------------------------------ page-selected decode
 
 @pytest.mark.parametrize("h_q", [1, 5, 16, 31, 33, 64, 65, 128, 130])
