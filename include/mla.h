@@ -416,7 +416,9 @@ MLA_API int mla_page_sparse_decode(const void* q, const void* kcache, int num_bl
  *                 its RoPE dims: they are normalised, then rotated
  *   kcache        [num_slots] rows of row_bytes bytes, row_bytes one of
  *     1152        576 bf16 (the dense cache)
- *     656         per 128 dims scale = absmax/448 (fp32; 1 for a zero group)
+ *     656         per 128 dims scale = absmax/448 (fp32; 1 for a zero group);
+ *                 codes are value * 448 / absmax, with the quotient unrounded
+ *                 (value / scale where the scale is below fp32's normal range)
  *     528         per 32 dims scale = the least power of two >= absmax/448
  *     288         per 16 dims scale = e4m3(absmax/6) (1 where that is 0)
  *                 codes are value / scale rounded to the nearest, ties to

@@ -10,7 +10,8 @@
 //                                                          (optional)
 //   1152 bytes  bf16(y)
 //    656 bytes  scale = absmax/448 per 128 dims (fp32, 1 for a zero group),
-//               codes e4m3(y / scale), the 64 RoPE dims in bf16
+//               codes e4m3(y 448 / absmax), the 64 RoPE dims in bf16
+//               (y / scale where the scale is not a normal fp32 number)
 //    528 bytes  scale = the least 2^e >= absmax/448 per 32 dims (E8M0)
 //    288 bytes  scale = e4m3(absmax/6) per 16 dims (1 where that is 0),
 //               codes e2m1(y / scale)
@@ -83,16 +84,30 @@ __device__ __forceinline__ double inv_root(double v) {
 // The same outside of it, kept out of line.
 __device__ __noinline__ double inv_root_far(double v) { return 1.0 / sqrt(v); }
 
-// y / scale for eight values.  kSmall: the scale may leave the range in which
-// its reciprocal serves.
-template <bool kSmall>
+// y / scale for eight values, of a scale between 2^-100 and 2^100.
 __device__ __forceinline__ void quotients8(const float* y, float scale, float* c) {
   const float inv = __frcp_rn(scale);
 #pragma unroll
   for (int k = 0; k < 8; ++k) c[k] = div_by(y[k], scale, inv);
-  if (kSmall && !(scale > 0x1p-100f && scale < 0x1p+100f)) {
+}
+
+// y 448 / amax for eight values of a group with maximum amax; y / scale where
+// scale = amax/448 is not a normal number.  One rounding where y is a bf16 value (the
+// product with 7/16 is exact, 1024 a power of two), and two such values whose quotient
+// is no rounding border of the codes lie 2^-13 of it away from one: the codes are then
+// the definition's, ties to even among them.  (y / scale takes the scale's rounding
+// along, by which some 45 codes in a million differed.)
+__device__ __forceinline__ void quotients8_of_max(const float* y, float amax, float scale,
+                                                  float* c) {
+  float n[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) c[k] = y[k] / scale;
+  for (int k = 0; k < 8; ++k) n[k] = y[k] * 0.4375f;
+  const float d = amax * 0x1p-10f;
+  quotients8(n, d, c);
+  if (!(d > 0x1p-100f && d < 0x1p+100f)) {
+    const bool normal = amax >= 448 * 0x1p-126f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c[k] = normal ? n[k] / amax * 1024.f : y[k] / scale;
   }
 }
 
@@ -207,8 +222,9 @@ __device__ __forceinline__ double amax_by_fp64(const double (&y)[8]) {
 }
 
 // Rarely called, by a whole warp, and kept out of line: a unit's codes as fp64 has them (E4M3 in .x
-// and .y, or E2M1 in .x; scale: as stored, the 656-byte rows take the group's own
-// absmax/448, unrounded), and the E4M3 code of absmax/6.
+// and .y, or E2M1 in .x; scale: as stored, in place of which the 656-byte rows take the
+// group's own absmax/448, unrounded, where that is a normal number), and the E4M3 code of
+// absmax/6.
 template <int kRowBytes>
 __device__ __noinline__ uint2 codes_by_fp64(uint4 raw, const float* gain, double inv, bool rotated,
                                             int position, double turns, float scale) {
@@ -216,7 +232,11 @@ __device__ __noinline__ uint2 codes_by_fp64(uint4 raw, const float* gain, double
   unit_by_fp64(raw, gain, inv, rotated, position, turns, y);
   if constexpr (kRowBytes == kRow656) {
     const double amax = amax_by_fp64<16>(y);
-    if (amax > 0.0) unit = amax / 448.0;
+    if (amax >= 448 * 0x1p-126) {
+      unit = amax;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] *= 448.0;
+    }
   }
   float c[8];
 #pragma unroll
@@ -349,7 +369,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
         // is decided in fp64.
         const bool rotated = !kWide && P.positions && j == 1;
         const float eps = rotated && lane >= 24 ? 0x1p-18f : P.gain ? 0x1p-21f : 0.f;
-        const float more = 1.f + eps, less = 1.f - eps;
+        float more = 1.f + eps, less = 1.f - eps;
         const float* gain = P.gain ? s_gain + u * 8 : nullptr;
         float amax = 0.f;
 #pragma unroll
@@ -373,7 +393,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
         } else if constexpr (kRowBytes == kRow656) {
           scale = amax > 0.f ? amax / 448.f : 1.f;
           if (!(scale > 0.f)) scale = 1.f;  // absmax/448 below the least fp32 value
-          quotients8<true>(y[j], scale, c);
+          quotients8_of_max(y[j], amax, scale, c);
+          if (scale < 0x1p-126f) {  // y / scale, rounded
+            more = 1.f + 0x1p-21f;
+            less = 1.f - 0x1p-21f;
+          }
           if (lane % kGroupLanes == 0)
             *reinterpret_cast<float*>(row + kNope + 4 * group) = scale;
         } else {
@@ -384,7 +408,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
             code = scale_by_fp64(raw[j], gain, inv, rotated, position, turns);
           if (code == 0) code = 0x38;  // 1.0, of a zero or tiny group
           scale = e4m3x2_to_float2(code).x;
-          quotients8<false>(y[j], scale, c);
+          quotients8(y[j], scale, c);
           if (lane % kGroupLanes == 0) row[kNope / 2 + group] = static_cast<uint8_t>(code);
         }
         if constexpr (kRowBytes == kRow288) {

@@ -250,6 +250,51 @@ def test_codes_are_those_of_fp64(fmt, rope):
     assert not wrong.any(), f"{int(wrong.sum())} codes differ"
 
 
+@pytest.mark.parametrize("fmt", ["656", "528", "288"])
+def test_codes_of_bf16_values_are_the_definitions(fmt):
+    """Without norm and rotation the values are bf16, products with 448 are exact in fp64 and a
+    quotient on a rounding border is formed exactly: every code has one value, ties to even."""
+    n, d, gen = 6000, width(fmt), torch.Generator().manual_seed(37)
+    kv = torch.randn((n, d), generator=gen).to(torch.bfloat16)
+    kv[:1000] = (kv[:1000].float() * 8).round().to(torch.bfloat16)  # maxima that 7 divides
+    kv[5000:] = (kv[5000:].float() * 2.0 ** -100).to(torch.bfloat16)
+    if fmt == "656":
+        kv[5500:, :512] = (kv[5500:, :512].float() * 2.0 ** -12).to(torch.bfloat16)
+        kv[5800:, :512] = (kv[5800:, :512].float() * 2.0 ** -9).to(torch.bfloat16)
+    cache = make_cache(fmt, n // 64 + 1, "cuda", gen)
+    B.mla_cache_append(kv.cuda(), torch.arange(n, dtype=torch.int32, device="cuda"), cache)
+    raw = raw_rows(cache)[:n]
+    y = kv[:, :512].double()
+    per = {"656": 128, "528": 32, "288": 16}[fmt]
+    g = y.reshape(n, 512 // per, per)
+    amax = g.abs().amax(2, keepdim=True)
+    if fmt == "288":
+        step = torch.exp2(torch.floor(torch.log2((amax / 6).clamp(min=2.0 ** -6))) - 3)
+        scale = torch.round(amax / 6 / step) * step
+        scale = torch.where(scale > 0, scale, 1.0)
+        assert torch.equal(e4m3(raw[:, 256:]), scale[..., 0])
+        v = (g / scale).reshape(n, 512)
+        step = torch.where(v.abs() < 2, 0.5, torch.where(v.abs() < 4, 1.0, 2.0)).double()
+        code = torch.stack([raw[:, :256] & 15, raw[:, :256] >> 4], 2).reshape(n, 512).long()
+        got = E2M1[code & 7] * torch.where(code >= 8, -1.0, 1.0)
+    else:
+        if fmt == "528":
+            scale = torch.exp2(raw[:, 512:].double() - 127)[..., None]
+            assert ((scale >= amax / 448) & (scale < amax / 224)).all()
+            v = g / scale
+        else:  # the stored scale counts below fp32's normal range
+            scale = raw[:, 512:528].contiguous().view(torch.float32).double()[..., None]
+            least = amax < 448 * 2.0 ** -126
+            assert least.any() and not least.all()
+            v = torch.where(least, g / scale, g * 448 / amax).clamp(-448, 448)
+        v = v.reshape(n, 512)
+        step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+        got = e4m3(raw[:, :512])
+    assert (v / step == torch.floor(v / step) + 0.5).any()  # ties are among them
+    want = torch.round(v / step) * step
+    assert torch.equal(got, want), f"{int((got != want).sum())} codes differ"
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_append_strided_rows_padding_and_no_rows_output(fmt):
     run(fmt, 77, stride=width(fmt) + 520, pad=(0, 5, 76), seed=4)
