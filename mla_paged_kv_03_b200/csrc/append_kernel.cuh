@@ -248,6 +248,25 @@ __device__ __noinline__ uint2 codes_by_fp64(uint4 raw, const float* gain, double
     return make_uint2(cvt_e4m3x4(c[0], c[1], c[2], c[3]), cvt_e4m3x4(c[4], c[5], c[6], c[7]));
   }
 }
+// Exponent e of the least power of two >= amax/448: amax = m 2^x with 1 <= m < 2 and
+// 448 = 1.75 * 2^8, so that e = x - 8, one more where m > 1.75; 0 of a zero group, -127
+// at least.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return amax > 0.f ? max(e, -127) : 0;  // at most 127 - 7 for a finite amax
+}
+// The same of a unit's group (4 lanes) from the latent.
+__device__ __noinline__ int scale_exponent_by_fp64(uint4 raw, const float* gain, double inv,
+                                                   bool rotated, int position, double turns) {
+  double y[8];
+  unit_by_fp64(raw, gain, inv, rotated, position, turns, y);
+  const double amax = amax_by_fp64<4>(y);
+  const unsigned long long bits = __double_as_longlong(amax);
+  const int e = static_cast<int>(bits >> 52) - 1023 - 8 +
+                ((bits & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull ? 1 : 0);
+  return amax > 0.0 ? max(min(e, 127 - 7), -127) : 0;
+}
 __device__ __noinline__ uint32_t scale_by_fp64(uint4 raw, const float* gain, double inv,
                                                bool rotated, int position, double turns) {
   double y[8];
@@ -380,11 +399,12 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
         float c[8];
         float scale;
         if constexpr (kRowBytes == kRow528) {
-          // amax = m 2^e with 1 <= m < 2, 448 = 1.75 * 2^8: the least power of
-          // two >= amax/448 is 2^(e - 8), one more where m > 1.75
-          const uint32_t bits = __float_as_uint(amax);
-          int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-          e = amax > 0.f ? max(e, -127) : 0;  // at most 127 - 7 for a finite amax
+          int e = scale_exponent(amax * more);
+          const bool near = e != scale_exponent(amax * less);
+          if (__any_sync(0xffffffffu, near)) {
+            const int exact = scale_exponent_by_fp64(raw[j], gain, inv, rotated, position, turns);
+            if (near) e = exact;
+          }
           scale = e8m0_to_float(static_cast<uint32_t>(e + 127));
           const float up = ldexpf(1.f, -e);  // exact: y * 2^-e is y / scale
 #pragma unroll

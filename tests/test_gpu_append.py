@@ -250,6 +250,35 @@ def test_codes_are_those_of_fp64(fmt, rope):
     assert not wrong.any(), f"{int(wrong.sum())} codes differ"
 
 
+@pytest.mark.parametrize("rope", [False, True])
+def test_528_scales_next_to_a_power_of_two(rope):
+    """Group maxima a few 2^-25 off 448 2^e, which fp32 rounds onto it: the scale is 2^e up to
+    there and 2^(e+1) above."""
+    wrong, sides = 0, set()
+    for seed in range(40):
+        gen = torch.Generator().manual_seed(seed)
+        x = (0.25 * torch.randn((1, 512), generator=gen).clamp(-3, 3)).to(torch.bfloat16)
+        x[:, ::32], x[:, 1::32] = 1.0, 0.0  # the maximum of each group; the dim it rotates with
+        pos = torch.randint(0, 1 << 17, (1,), generator=gen, dtype=torch.int32) if rope else None
+        # the gains that bring those next to 3.5, up to two steps of fp32 away
+        y, _ = expected(x, pos, torch.ones(512), 0.0, 1e4)
+        top = torch.maximum(y[0, ::32].abs(), y[0, 1::32].abs())
+        gain = torch.ones(512)
+        near = (3.5 / top).float()
+        gain[::32] = (near.view(torch.int32) + torch.arange(16, dtype=torch.int32) % 5 - 2).view(
+            torch.float32)
+        y, _ = expected(x, pos, gain, 0.0, 1e4)
+        amax = y.reshape(16, 32).abs().amax(1)
+        assert ((amax / 3.5 - 1).abs() < 2.0 ** -21).all()
+        sides |= {bool(v) for v in amax > 3.5}
+        cache = make_cache("528", 1, "cuda", gen)
+        B.mla_cache_append(x.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda"), cache,
+                           positions=pos.cuda() if rope else None, norm_gain=gain.cuda(), eps=0.0)
+        got = raw_rows(cache)[0, 512:].int() - 127
+        wrong += int((got != torch.where(amax > 3.5, -6, -7)).sum())
+    assert len(sides) == 2 and wrong == 0, f"{wrong} scales differ"
+
+
 @pytest.mark.parametrize("fmt", ["656", "528", "288"])
 def test_codes_of_bf16_values_are_the_definitions(fmt):
     """Without norm and rotation the values are bf16, products with 448 are exact in fp64 and a
