@@ -675,8 +675,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) mla_page_select_kernel(const P
 #pragma unroll
           for (int g = 0; g < kSelHeads / 32; ++g)
             if (32 * g < nh) v = fmaxf(v, s_best[g][tid]);
-          // + 0: a product that underflows to -0 ties with 0
-          scores[p] = final_pass ? max(order_key(v * key_scale + 0.f), 1u) : __float_as_uint(v);
+          // + 0: a product that underflows to -0 ties with 0 (of one fma it would stay -0)
+          scores[p] = final_pass
+                          ? max(order_key(__fadd_rn(__fmul_rn(v, key_scale), 0.f)), 1u)
+                          : __float_as_uint(v);
         }
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");

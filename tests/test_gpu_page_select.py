@@ -304,6 +304,18 @@ def test_zero_query_and_equal_products():
     assert c.run(4)[2].cpu().tolist() == [[[0, 1, 2, 12]]]
 
 
+@pytest.mark.parametrize("h_q", [1, 130])
+def test_scores_that_underflow_tie_with_zero(h_q):
+    # negative products that underflow on the even pages, exact zeros on the odd ones
+    c = Case([64 * 12], h_q=h_q, seed=26)
+    c.q[:] = 2.0 ** -100
+    c.keys[:] = 0
+    c.keys[c.table[0, 0:12:2].long()] = -1
+    c.scales[:] = 2.0 ** -90
+    assert c.run(5)[2].cpu().tolist() == [[[0, 1, 2, 3, 11]]]
+    c.check(c.run(5), 5)
+
+
 def test_negative_scores_are_ordered():
     c = Case([64 * 40], h_q=1, seed=11)
     base = torch.randint(1, 127, (576,), dtype=torch.int8)
