@@ -9,7 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
-#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -129,17 +129,22 @@ at::Tensor workspace(PyObject* o, size_t bytes, at::Device device) {
   return t;
 }
 
+// The GIL, free for the life of this object: an exception that leaves it takes it back.
+struct FreeGil {
+  PyThreadState* state = PyEval_SaveThread();
+  ~FreeGil() { PyEval_RestoreThread(state); }
+};
+
 // call(stream) with device `index` current, on its current stream; the GIL is
-// free meanwhile, as in a ctypes call.
+// free meanwhile, as in a ctypes call.  (What torch does here throws on a CUDA error.)
 template <class Call>
 void launch(int index, Call call) {
   int rc;
-  Py_BEGIN_ALLOW_THREADS;
-  const int before = c10::cuda::current_device();
-  if (before != index) c10::cuda::set_device(static_cast<c10::DeviceIndex>(index));
-  rc = call(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
-  if (before != index) c10::cuda::set_device(static_cast<c10::DeviceIndex>(before));
-  Py_END_ALLOW_THREADS;
+  {
+    FreeGil free_gil;
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+    rc = call(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
+  }
   if (rc != MLA_OK) throw LibraryError{rc};
 }
 

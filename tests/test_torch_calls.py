@@ -1,5 +1,8 @@
 """Argument checks of the cache-side calls that need no GPU: CPU tensors, other
 objects and wrong counts are refused with a Python error."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -48,3 +51,30 @@ def test_counts_of_arguments():
             f()
         with pytest.raises(TypeError):
             f(*[None] * 30)
+
+
+# Tensors that name a CUDA device without having any memory: the call gets as far as the
+# device, where torch throws.  A process of its own, which used to end with a fault there.
+AT_THE_DEVICE = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from mla_paged_kv_03_b200 import binding as B
+B.calls()
+with FakeTensorMode():
+    cuda = dict(device="cuda:63")
+    args = (torch.empty((2, 64, 1, 576), dtype=torch.bfloat16, **cuda),
+            torch.empty((1, 2), dtype=torch.int32, **cuda),
+            torch.empty(1, dtype=torch.int32, **cuda),
+            torch.empty((2, 576), dtype=torch.int8, **cuda), torch.empty(2, **cuda))
+for _ in range(2):
+    try:
+        B.mla_page_keys_update(*args)
+    except Exception as e:
+        print("raised", type(e).__name__)
+"""
+
+
+def test_an_error_of_the_device_is_an_exception():
+    r = subprocess.run([sys.executable, "-c", AT_THE_DEVICE], capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+    assert r.stdout.split().count("raised") == 2
