@@ -211,12 +211,14 @@ struct UnitIter {
       u.L_raw = L_raw;
       // A length beyond the block table's max_pages * 64 tokens is read as
       // that many (the block table names no further page) and recorded as an
-      // input fault; tiles past it are fully masked, so every split the
-      // planner counted still writes its (empty) partial.
+      // input fault; of the tiles past it, which are fully masked, a split takes
+      // its first if it has no other, so that every split the planner counted
+      // still writes its (empty) partial.
       u.L = L_raw;
       if (!prefix && L_raw > P.max_pages * kPage) {
         ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x30);
         u.L = P.max_pages * kPage;
+        u.hi = min(hi, max(lo + 1, tiles_of(u.L)));
       }
       return true;
     }

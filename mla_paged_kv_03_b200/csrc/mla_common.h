@@ -98,14 +98,19 @@ MLA_HD inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Tiles (of 128 tokens) a sequence of length L contributes.  An empty
 // sequence still owns one (fully masked) tile so that some CTA writes its
-// O = 0, LSE = -inf result.
-MLA_HD inline int tiles_of(int L) { return L > 0 ? ceil_div(L, kTileT) : 1; }
+// O = 0, LSE = -inf result.  (No cache holds kMaxTokens: lengths past it count
+// as that many, so that neither the sum here nor tiles * kTileT overflows.)
+constexpr int kMaxTokens = 0x7fffffff - (kTileT - 1);
+MLA_HD inline int tiles_of(int L) {
+  return L > 0 ? ceil_div(L < kMaxTokens ? L : kMaxTokens, kTileT) : 1;
+}
 
 // Planner granules (of g tiles) a sequence of length L contributes.
 MLA_HD inline int granules_of(int L, int g) { return (tiles_of(L) + g - 1) / g; }
 
 // The planner counts in int32: the total cost sum(tiles + overhead) of a
-// call must stay below this (checked by the entry points).
+// call must stay below this (checked by the entry points that know the lengths;
+// the device planner cuts lengths that pass it and records them as an input fault).
 constexpr long long kPlanMaxTotal = (1LL << 30);
 
 // ------------------------------------------------------- split-KV planner

@@ -1,0 +1,83 @@
+"""Lengths that no cache holds (uninitialised ones, say): the planner's sums stay within int32, the
+splits within the workspace, and a decode takes such a length as the block table's end without
+walking the tiles behind it."""
+import pytest
+import torch
+
+from mla_paged_kv_03_b200 import binding as B
+from mla_paged_kv_03_b200 import workloads as W
+from parity_util import assert_lse_close, assert_out_close
+from test_gpu_faults import DENSE_SHAPES, dense_gpu, dense_oracle
+from test_gpu_shared_prefix import Case
+
+pytestmark = pytest.mark.gpu
+
+MOST = 2 ** 31 - 1
+
+
+def assert_plan_in_bounds(meta, ns, batch, parts):
+    meta, ns = meta.cpu(), ns.cpu()
+    steps = ns[1:] - ns[:-1]
+    assert ns[0] == 0 and (steps >= 1).all() and ns[-1] <= batch + parts
+    live = meta[:, 0] <= meta[:, 2]
+    assert live.any()
+    assert (meta[live, 0] >= 0).all() and (meta[live, 2] < batch).all()
+    assert (meta[live, 1] >= 0).all() and (meta[live, 3] >= 1).all()
+    assert (meta[live, 4] >= 0).all() and (meta[live, 4] < steps[meta[live, 0].long()]).all()
+
+
+@pytest.mark.parametrize("heads", [16, 64, 128])
+@pytest.mark.parametrize("lengths", [[MOST] * 40 + [100], [MOST], [100, MOST] * 500,
+                                     [5_000_000] * 8192, [MOST - 127] * 33 + [MOST - 128] * 7])
+def test_plans_of_far_lengths(heads, lengths):
+    B.device_status(reset=True)
+    sl = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    meta, ns, parts = B.mla_get_metadata(sl, heads, 1)
+    torch.cuda.synchronize()
+    assert_plan_in_bounds(meta, ns, len(lengths), parts)
+    code = B.device_status() >> 16
+    assert code == (0 if len(lengths) == 1 else B.MLA_DEVERR_BAD_INDEX)
+
+
+@pytest.mark.parametrize("heads", [16, 64, 128])
+def test_long_lengths_that_fit_are_planned_as_on_the_host(heads):
+    # one sequence with more than its share, and a sum below the limit
+    lengths = [1 << 28, 70, 0, 1 << 24] + [130] * 300
+    meta, ns, parts = B.mla_get_metadata(torch.tensor(lengths, dtype=torch.int32, device="cuda"),
+                                         heads, 1)
+    hm, hn = B.mla_get_metadata_host(lengths, heads, parts)
+    assert torch.equal(meta.cpu(), hm) and torch.equal(ns.cpu(), hn)
+    assert B.device_status() == 0
+
+
+@pytest.mark.parametrize("s_q,h_q,d_v", DENSE_SHAPES)
+@pytest.mark.parametrize("far", [1 << 20, MOST - 200, MOST])
+def test_dense_decode_of_far_lengths(s_q, h_q, d_v, far):
+    B.device_status(reset=True)
+    case = W.make_dense([700, 130, 64], s_q, h_q, seed=51, d_v=d_v, spare_blocks=1)
+    sl = torch.tensor([far, 130, far], dtype=torch.int32)
+    bt = case.block_table.clone()
+    bt[bt < 0] = 0
+    out, lse = dense_gpu(case, bt=bt, sl=sl)
+    torch.cuda.synchronize()
+    assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+    ro, rl = dense_oracle(case, bt=bt, sl=torch.tensor([bt.shape[1] * 64, 130, bt.shape[1] * 64],
+                                                       dtype=torch.int32))
+    assert_out_close(out, ro)
+    assert_lse_close(lse, rl)
+
+
+@pytest.mark.parametrize("far", [1 << 20, MOST])
+@pytest.mark.parametrize("h_q", [16, 128])
+def test_shared_prefix_decode_of_far_lengths(h_q, far):
+    B.device_status(reset=True)
+    c = Case([70, 64, 128], 700, 2, h_q, seed=52)
+    t = list(c.dev())
+    t[4] = torch.tensor([far, 64, far], dtype=torch.int32, device="cuda")
+    c.table[c.table < 0] = 0
+    t[3] = c.table.cuda()
+    got = c.run(t=t)
+    torch.cuda.synchronize()
+    assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+    c.lengths = [128, 64, 128]
+    c.check(got)
