@@ -291,11 +291,10 @@ __device__ __forceinline__ int clamp_block(int blk, int num_blocks) {
 // the rows before the page's first with zeros, the n rows follow, and none behind
 // them is read.  Slot t of such a page is token t - page_shift of the page, and
 // no token for t < page_shift.  (The maps have the rows of a page in a dimension
-// of their own, so that rows -64 .. -1 are outside of it.)
-// 0 for a page that the sequence does not reach, which is masked whole.
+// of their own, so that rows -64 .. -1 are outside of it.)  64 for a page that the
+// sequence does not reach, which is zeros and masked whole.
 __device__ __forceinline__ int page_shift(int L, int page) {
-  const int n = L - page * kPage;
-  return n > 0 && n < kPage ? kPage - n : 0;
+  return min(max(kPage - (L - page * kPage), 0), kPage);
 }
 
 // --------------------------------------------------------------------------
@@ -395,9 +394,7 @@ __global__ void __launch_bounds__(Threads<kMode>::value, 1)
       int blk1 = (p0 + 1 < npg) ? P.block_table[(size_t)un.b * P.max_pages + p0 + 1] : blk0;
       blk0 = clamp_block(blk0, P.num_blocks);
       blk1 = clamp_block(blk1, P.num_blocks);
-      // an empty sequence loads zeros
-      const int y0 = un.L > 0 ? -page_shift(un.L, p0) : -kPage;
-      const int y1 = p0 + 1 < npg ? -page_shift(un.L, p0 + 1) : y0;
+      const int y0 = -page_shift(un.L, p0), y1 = -page_shift(un.L, p0 + 1);
       if (P.trace && pair == 0) {
         if (p0 < npg) trace_page(P, un.b, p0, blk0, planes);
         if (p0 + 1 < npg) trace_page(P, un.b, p0 + 1, blk1, planes);

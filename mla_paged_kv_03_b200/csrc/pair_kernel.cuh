@@ -225,10 +225,10 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
     return clamp_block(blk, P.num_blocks);
   };
   // First row of the load of logical page `page`, or of the page that stands in
-  // for it (page_shift; an empty sequence loads zeros).
+  // for it (page_shift).
   auto page_row0 = [&](const Unit& un, int page, int fallback) -> int {
     const int end = min((un.L + kPage - 1) / kPage, 2 * un.hi);
-    return un.L > 0 ? -page_shift(un.L, page < end ? page : fallback) : -kPage;
+    return -page_shift(un.L, page < end ? page : fallback);
   };
   // Gather mode: the row of index entry e of unit `un` (row 0, masked, for an
   // entry past the unit's length or naming no row).
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(pcfg::kThreads, 1)
         int shift = 0;
         if constexpr (!kGather) {
           shift = page_shift(u.L, 2 * u.lo + 4 * i + quarter);
-          nvalid = nvalid > 0 ? nvalid + shift : 0;
+          nvalid = nvalid > 0 ? nvalid + shift : 0;  // (never of an unreached page)
         }
         // One pass with the running maximum m: P = 2^(scale*s - m).  When some
         // row's maximum exceeds m_used by more than the threshold (always on a

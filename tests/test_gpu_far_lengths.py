@@ -81,3 +81,25 @@ def test_shared_prefix_decode_of_far_lengths(h_q, far):
     assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
     c.lengths = [128, 64, 128]
     c.check(got)
+
+
+@pytest.mark.parametrize("s_q,h_q,d_v", DENSE_SHAPES)
+@pytest.mark.parametrize("past", [1, 64, 300, 5000])
+def test_a_length_past_the_table_does_not_read_block_0(s_q, h_q, d_v, past):
+    # block 0 is nobody's and holds NaN; the splits planned for the tiles past the table are empty
+    B.device_status(reset=True)
+    case = W.make_dense([640, 130], s_q, h_q, seed=53, d_v=d_v, spare_blocks=2)
+    bt = case.block_table
+    spare = [i for i in range(case.kcache.shape[0]) if i not in bt.flatten().tolist()]
+    if 0 not in spare:
+        case.kcache[spare[0]] = case.kcache[0]
+        bt[bt == 0] = spare[0]
+    case.kcache[0] = float("nan")
+    sl = torch.tensor([640 + past, 130], dtype=torch.int32)
+    out, lse = dense_gpu(case, bt=bt, sl=sl)
+    torch.cuda.synchronize()
+    assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+    case.kcache[0] = 0
+    ro, rl = dense_oracle(case, bt=bt)
+    assert_out_close(out, ro)
+    assert_lse_close(lse, rl)
