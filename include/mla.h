@@ -510,8 +510,7 @@ MLA_API int mla_set_slot_trace(int32_t* trace, int64_t capacity);
 /* Reads the device status words that kernels set: 0 = ok, else (code << 16)
  * | site of the first event, code 1 = a bounded wait expired, 2 = an input
  * named nothing in the cache (a block id outside [0, num_blocks), a length
- * above max_pages * 64 or lengths that add up to more than about 2^35 tokens,
- * a sparse index outside [0, num_slots)).  A code-2
+ * above max_pages * 64, a sparse index outside [0, num_slots)).  A code-2
  * fault does not stop any kernel: the block id reads block 0, the length is
  * cut to max_pages * 64 (the default fused query position still follows the
  * length as given), and the index is skipped like -1.  A timeout makes every

@@ -12,7 +12,6 @@
 // saturating).  [FlashMLA fused norm-RoPE-attention-RoPE-cast kernel card]
 #pragma once
 #include <cuda_bf16.h>
-#include <climits>
 #include <cstdint>
 
 #include "mla_common.h"
@@ -285,35 +284,18 @@ __device__ void plan_block(const Lengths seqlens, int batch, int num_parts, cons
   const int o = pp.o, g = pp.g;
   const int u = g * kPlanTileCost;
   const int tid = threadIdx.x;
-  const int share = static_cast<int>(kPlanMaxTotal) / max(batch, 1);
   int carry = 0;
-  for (int most = INT_MAX;;) {  // granules that a sequence counts for
-    long long mine = 0;
-    bool much = false;
-    carry = 0;
-    for (int base = 0; base < batch; base += kThreads) {
-      const int b = base + tid;
-      const int L = b < batch ? seqlens(b) : 0;
-      const int v = b < batch ? o + u * min(granules_of(L, g), most) : 0;
-      mine += v;
-      much |= v > share;
-      int chunk_total;
-      const int ex = block_exclusive_scan<kThreads>(v, &chunk_total);
-      if (b < batch) C[b] = carry + ex;
-      carry += chunk_total;
-    }
-    if (tid == 0) C[batch] = carry;
-    // with no cost above an equal share of what int32 holds, their sum fits
-    if (!__syncthreads_or(much)) break;
-    __shared__ unsigned long long s_total;
-    if (tid == 0) s_total = 0;
-    __syncthreads();
-    atomicAdd(&s_total, static_cast<unsigned long long>(mine));
-    __syncthreads();
-    if (s_total <= kPlanMaxTotal) break;
-    if (tid == 0) ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x7b);
-    most = (share - o) / u;
+  for (int base = 0; base < batch; base += kThreads) {
+    const int b = base + tid;
+    const int L = b < batch ? seqlens(b) : 0;
+    const int v = b < batch ? o + u * min(granules_of(L, g), pp.most) : 0;
+    int chunk_total;
+    const int ex = block_exclusive_scan<kThreads>(v, &chunk_total);
+    if (b < batch) C[b] = carry + ex;
+    carry += chunk_total;
   }
+  if (tid == 0) C[batch] = carry;
+  __syncthreads();
   const int w = plan_width(carry, num_parts, pp);
   for (int p = tid; p < num_parts; p += kThreads)
     plan_part_row(C, batch, w, o, g, p, metadata + p * kMetaInts);

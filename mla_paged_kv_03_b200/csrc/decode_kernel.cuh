@@ -201,13 +201,14 @@ struct UnitIter {
       }
       const int lo = (bb == b_first) ? t_begin : 0;
       const int tiles = tiles_of(L_raw);  // the planner's tiles
-      const int hi = (bb == b_end) ? min(t_end, tiles) : tiles;
+      u.split = (bb == b_first) ? s_begin : 0;
+      u.nsplit = P.num_splits[bb + 1] - P.num_splits[bb];
+      // (a sequence's last split ends with it, whatever the planner counted it for)
+      const int hi = bb == b_end && u.split < u.nsplit - 1 ? min(t_end, tiles) : tiles;
       if (lo >= hi) continue;
       u.b = bb;
       u.lo = lo;
       u.hi = hi;
-      u.split = (bb == b_first) ? s_begin : 0;
-      u.nsplit = P.num_splits[bb + 1] - P.num_splits[bb];
       u.L_raw = L_raw;
       // A length beyond the block table's max_pages * 64 tokens is read as
       // that many (the block table names no further page) and recorded as an

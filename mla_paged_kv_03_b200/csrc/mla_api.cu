@@ -744,7 +744,7 @@ int mla_get_metadata(const int32_t* cache_seqlens, int batch, int heads_per_kv, 
   MLA_CHECK_ARG(batch <= mla::kPlanMaxBatch, "the device planner takes at most %d sequences (got %d)",
                 mla::kPlanMaxBatch, batch);
   mla::mla_plan_kernel<<<1, mla::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      cache_seqlens, batch, num_sm_parts, mla::plan_params(heads_per_kv), metadata, num_splits,
+      cache_seqlens, batch, num_sm_parts, mla::plan_params(heads_per_kv, batch), metadata, num_splits,
       nullptr, nullptr, 0);
   MLA_CUDA(cudaGetLastError());
   return MLA_OK;
@@ -758,12 +758,13 @@ int mla_get_metadata_host(const int32_t* cache_seqlens, int batch, int heads_per
   MLA_CHECK_ARG(metadata && num_splits && (cache_seqlens || batch == 0), "null host pointer");
   for (int b = 0; b < batch; ++b)
     MLA_CHECK_ARG(cache_seqlens[b] >= 0, "cache_seqlens[%d] = %d is negative", b, cache_seqlens[b]);
-  const mla::PlanParams pp = mla::plan_params(heads_per_kv);
+  const mla::PlanParams pp = mla::plan_params(heads_per_kv, batch);
   std::vector<int32_t> granules(static_cast<size_t>(batch));
   long long total = 0;
   for (int b = 0; b < batch; ++b) {
     granules[b] = mla::granules_of(cache_seqlens[b], pp.g);
     total += pp.o + static_cast<long long>(mla::kPlanTileCost) * pp.g * granules[b];
+    if (granules[b] > pp.most) granules[b] = pp.most;
   }
   MLA_CHECK_ARG(total <= mla::kPlanMaxTotal, "total planner cost %lld above %lld", total,
                 mla::kPlanMaxTotal);
@@ -1036,7 +1037,7 @@ int mla_sparse_prefill_fwd(const void* q, const void* kv, int64_t s_kv, const in
         topk_length ? topk_length + t0 : nullptr, topk, n, lengths);
     MLA_CUDA(cudaGetLastError());
     mla::mla_plan_kernel<<<1, mla::kPlanThreads, 0, st>>>(
-        lengths, n, parts, mla::plan_params(h_q), meta, splits, base, split_list, parts);
+        lengths, n, parts, mla::plan_params(h_q, n), meta, splits, base, split_list, parts);
     MLA_CUDA(cudaGetLastError());
     mla::DecodeParams p{};
     p.batch = n;
@@ -1187,7 +1188,7 @@ int mla_shared_prefix_get_metadata(const int32_t* cache_seqlens, int batch, int 
                 "int32 arrays must be 4-byte aligned");
   mla::mla_shared_plan_kernel<<<1, mla::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       cache_seqlens, su.units, su.n_prefix, prefix_len, su.own_groups, rows_per_kv, num_sm_parts,
-      mla::plan_params_shared(rows_per_kv), metadata, num_splits);
+      mla::plan_params_shared(rows_per_kv, su.units), metadata, num_splits);
   MLA_CUDA(cudaGetLastError());
   return MLA_OK;
 }
@@ -1407,7 +1408,7 @@ int mla_page_sparse_decode(const void* q, const void* kcache, int num_blocks,
   // and 128 parts: 56.1 and 54.2.
   const int parts = pairs <= num_sm_parts ? num_sm_parts / pairs * pairs : num_sm_parts;
   p.num_parts = parts;
-  p.plan = mla::plan_params(h_q);
+  p.plan = mla::plan_params(h_q, pairs);
   p.metadata = meta;
   p.num_splits = splits;
   MLA_CUDA(allow_smem<mla::mla_page_select_kernel>(mla::select_smem(mla::kSelHeads, 0)));

@@ -58,14 +58,27 @@ constexpr int kPlanOverheadPair = MLA_PLAN_OVH_PAIR;  // > 64 rows (CTA-pair ker
 constexpr int kPlanMinWidthCta = 2 * kPlanTileCost;
 
 // The planner's constants for the kernel that serves `heads_per_kv` rows:
-// segment overhead o, granule g (tiles) and minimum part width (cost units).
+// segment overhead o, granule g (tiles) and minimum part width (cost units), and
+// the granules that a sequence of the batch counts for at most.
 struct PlanParams {
-  int o, g, wmin;
+  int o, g, wmin, most;
 };
-MLA_HD inline PlanParams plan_params(int heads_per_kv) {
-  if (heads_per_kv <= 32) return {kPlanOverheadPage, 1, 0};
-  if (heads_per_kv <= 64) return {kPlanOverheadCta, 1, kPlanMinWidthCta};
-  return {kPlanOverheadPair, 2, 0};
+
+// The planner counts in int32: the total cost sum(tiles + overhead) of a
+// call must stay below this (checked by the entry points that know the lengths).
+// So that no lengths, uninitialised ones either, overflow the sums, a sequence counts
+// for an equal share of it at most (4 million tokens at the largest batch of 8192);
+// its last split takes the tiles past that.
+constexpr long long kPlanMaxTotal = (1LL << 30);
+
+inline PlanParams plan_params(int o, int g, int wmin, int batch) {
+  const int share = static_cast<int>(kPlanMaxTotal / (batch > 0 ? batch : 1));
+  return {o, g, wmin, (share - o) / (g * kPlanTileCost)};
+}
+inline PlanParams plan_params(int heads_per_kv, int batch) {
+  if (heads_per_kv <= 32) return plan_params(kPlanOverheadPage, 1, 0, batch);
+  if (heads_per_kv <= 64) return plan_params(kPlanOverheadCta, 1, kPlanMinWidthCta, batch);
+  return plan_params(kPlanOverheadPair, 2, 0, batch);
 }
 
 // Of a shared-prefix decode with `rows_per_kv` query rows per sequence.  What a
@@ -74,8 +87,9 @@ MLA_HD inline PlanParams plan_params(int heads_per_kv) {
 // sequences behind 16384 tokens 279 and 248; 64 rows, 100 behind 8000 136 and
 // 119; 32 rows, 128 behind 8000 87 and 91; 8 rows, 200 behind 8000 66 and 75.
 constexpr int kPlanOverheadShared = 16, kPlanOverheadSharedFewRows = 8;
-MLA_HD inline PlanParams plan_params_shared(int rows_per_kv) {
-  return {rows_per_kv > 32 ? kPlanOverheadShared : kPlanOverheadSharedFewRows, 2, 0};
+inline PlanParams plan_params_shared(int rows_per_kv, int units) {
+  return plan_params(rows_per_kv > 32 ? kPlanOverheadShared : kPlanOverheadSharedFewRows, 2, 0,
+                     units);
 }
 
 // By entries 5 (this), 6 (prefix length) and 7 (rows per KV head) of each metadata
@@ -98,20 +112,11 @@ MLA_HD inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Tiles (of 128 tokens) a sequence of length L contributes.  An empty
 // sequence still owns one (fully masked) tile so that some CTA writes its
-// O = 0, LSE = -inf result.  (No cache holds kMaxTokens: lengths past it count
-// as that many, so that neither the sum here nor tiles * kTileT overflows.)
-constexpr int kMaxTokens = 0x7fffffff - (kTileT - 1);
-MLA_HD inline int tiles_of(int L) {
-  return L > 0 ? ceil_div(L < kMaxTokens ? L : kMaxTokens, kTileT) : 1;
-}
+// O = 0, LSE = -inf result.  (No sum that the largest lengths overflow.)
+MLA_HD inline int tiles_of(int L) { return L > 0 ? (L - 1) / kTileT + 1 : 1; }
 
 // Planner granules (of g tiles) a sequence of length L contributes.
 MLA_HD inline int granules_of(int L, int g) { return (tiles_of(L) + g - 1) / g; }
-
-// The planner counts in int32: the total cost sum(tiles + overhead) of a
-// call must stay below this (checked by the entry points that know the lengths;
-// the device planner cuts lengths that pass it and records them as an input fault).
-constexpr long long kPlanMaxTotal = (1LL << 30);
 
 // ------------------------------------------------------- split-KV planner
 //
