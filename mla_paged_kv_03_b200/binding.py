@@ -597,7 +597,8 @@ def mla_cache_append(kv: torch.Tensor, slots: torch.Tensor, kcache: torch.Tensor
     kv [n, 576] bf16 for a bf16 cache [NB, 64, 1, 576] or a 656-byte one (uint8
     [..., 656]), [n, 512] for the 528- and 288-byte ones; its rows may be
     strided.  slots [n] int32 physical slots (negative = padding, skipped; the
-    others must differ).  `rows` (bf16, kv's shape, contiguous) receives the
+    others must differ); slots and positions may be int64 (values past int32
+    count as its limits).  `rows` (bf16, kv's shape, contiguous) receives the
     rows as the cache stands for them.  Writes into `kcache`; returns `rows`."""
     return (_calls or calls()).cache_append(kv, slots, kcache, positions, norm_gain, eps,
                                             rope_base, rows)

@@ -77,12 +77,16 @@ bool truth(PyObject* o) {
   return v != 0;
 }
 
-// `t` as a contiguous int32 tensor on device `index`.
+// `t` as a contiguous int32 tensor on device `index`.  An int64 value past int32 becomes
+// the nearest int32: out of the cache's or the table's range as it was (a cast would wrap
+// it onto another index).
 at::Tensor int32_on(const at::Tensor& t, const char* name, int index) {
   require(t.is_cuda() && t.get_device() == index, name, "a tensor", index);
   if (t.scalar_type() != at::kInt) {
     require(t.scalar_type() == at::kLong, name, "int32 (or int64)", index);
-    return t.to(at::kInt).contiguous();
+    return t.clamp(std::numeric_limits<int>::min(), std::numeric_limits<int>::max())
+        .to(at::kInt)
+        .contiguous();
   }
   return t.contiguous();
 }

@@ -393,6 +393,23 @@ def test_append_bad_slots_are_skipped_and_recorded():
     assert torch.equal(cache.view(128, 576), want)
 
 
+def test_int64_slots_past_int32_are_out_of_range():
+    # 2^32 + 5 is not slot 5
+    dev = torch.device("cuda")
+    kv = torch.ones((6, 576), dtype=torch.bfloat16, device=dev)
+    kv[5] = 2.0
+    cache = torch.zeros((2, 64, 1, 576), dtype=torch.bfloat16, device=dev)
+    B.mla_cache_append(kv, torch.tensor([-1, -2 ** 32 + 5, -2 ** 63, -7, -2 ** 31 - 2 ** 32, 127],
+                                        device=dev), cache)
+    assert B.device_status() == 0  # padding
+    B.mla_cache_append(kv, torch.tensor([2 ** 32 + 5, 2 ** 31, 2 ** 63 - 1, 2 ** 32, -1, 127],
+                                        device=dev), cache)
+    assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+    want = torch.zeros((128, 576), dtype=torch.bfloat16, device=dev)
+    want[127] = 2.0
+    assert torch.equal(cache.view(128, 576), want)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_append_keeps_non_finite_rows_apart(fmt):
     dev = torch.device("cuda")

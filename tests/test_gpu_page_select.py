@@ -460,6 +460,31 @@ def test_wider_indexes_and_strided_inputs():
     assert torch.equal(keys.cpu()[owned], c.keys[owned])
 
 
+def test_int64_blocks_and_lengths_past_int32_are_out_of_range():
+    c = Case([500, 450], seed=20)
+    keys, scales = c.keys.cuda(), c.scales.cuda()
+    args = (c.q.cuda(), c.cache.cuda(), keys, scales)
+    table, sl = c.table.long(), c.sl().long()
+    table[0, 2] += 2 ** 32
+    got = B.mla_page_sparse_decode(*args, table.cuda(), sl, 8, softmax_scale=c.scale)
+    assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+    good, c.table[0, 2] = int(c.table[0, 2]), 0  # block 0 stands in for it
+    c.check(got, 8)
+    # its key is not written
+    keys[:] = 99
+    B.mla_page_keys_update(c.cache.cuda(), table.cuda(), sl, keys, scales)
+    assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+    assert (keys[good] == 99).all()
+    # a length of 2^32 + 450 is past the table, not 450
+    c.table[0, 2] = good
+    sl[1] += 2 ** 32
+    got = B.mla_page_sparse_decode(*args[:2], c.keys.cuda(), c.scales.cuda(), c.table.cuda(), sl, 3,
+                                   softmax_scale=c.scale)
+    assert B.device_status() >> 16 == B.MLA_DEVERR_BAD_INDEX
+    c.lengths = [500, 512]
+    c.check(got, 3)
+
+
 def test_two_streams_at_once():
     a, b = Case([64 * 150 + 3] * 3, h_q=128, seed=23), Case([5000, 64], h_q=16, seed=24)
     ta = (a.q.cuda(), a.cache.cuda(), a.keys.cuda(), a.scales.cuda(), a.table.cuda(), a.sl())
