@@ -313,6 +313,7 @@ PyObject* page_keys_update(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const PageArgs p = page_args(a[0], a[3], a[4], a[1], a[2], index);
     require(cache.size(2) == 1, "kcache must be [NB, 64, 1, 576]");
     const int tail = a[5] == Py_None ? p.max_pages : whole32(a[5]);
+    if (p.batch == 0) Py_RETURN_NONE;  // (empty tensors have no address)
     launch(index, [&](cudaStream_t stream) {
       return mla_page_keys_update(cache.data_ptr(), p.blocks,
                                   static_cast<const int32_t*>(p.table.data_ptr()), p.max_pages,
@@ -347,6 +348,7 @@ PyObject* page_sparse_decode(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const at::Tensor lse = output(a[13], "lse", {b, s_q, h_q}, at::kFloat, dev);
     const at::Tensor pages = output(a[11], "pages", {b, s_q, topk}, at::kInt, dev);
     const at::Tensor ws = workspace(a[14], bytes, dev);
+    if (b == 0) return pack({out, lse, pages});
     const float scale = softmax_scale(a[8]);
     const bool causal = truth(a[7]);
     launch(index, [&](cudaStream_t stream) {
@@ -412,6 +414,7 @@ PyObject* shared_prefix_decode(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     const at::Tensor out = output(a[11], "out", {b, s_q, h_q, kNope}, at::kBFloat16, dev);
     const at::Tensor lse = output(a[12], "lse", {b, s_q, h_q}, at::kFloat, dev);
     const at::Tensor ws = workspace(a[13], bytes, dev);
+    if (b == 0) return pack({out, lse});
     const float scale = softmax_scale(a[10]);
     const bool causal = truth(a[9]);
     launch(index, [&](cudaStream_t stream) {

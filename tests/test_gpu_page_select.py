@@ -460,6 +460,15 @@ def test_wider_indexes_and_strided_inputs():
     assert torch.equal(keys.cpu()[owned], c.keys[owned])
 
 
+def test_an_empty_batch():
+    c = Case([500], seed=27)
+    none = c.table[:0].cuda()
+    got = B.mla_page_sparse_decode(c.q[:0].cuda(), c.cache.cuda(), c.keys.cuda(), c.scales.cuda(),
+                                   none, c.sl()[:0], 3)
+    assert [tuple(t.shape) for t in got] == [(0, 1, 16, 512), (0, 1, 16), (0, 1, 3)]
+    B.mla_page_keys_update(c.cache.cuda(), none, c.sl()[:0], c.keys.cuda(), c.scales.cuda())
+
+
 def test_int64_blocks_and_lengths_past_int32_are_out_of_range():
     c = Case([500, 450], seed=20)
     keys, scales = c.keys.cuda(), c.scales.cuda()

@@ -283,6 +283,16 @@ def test_a_short_num_splits_is_refused():
     assert_refused(c, (meta, ns[:1].clone(), n))
 
 
+@pytest.mark.parametrize("prefix_len", [0, 130])
+def test_an_empty_batch(prefix_len):
+    c = Case([70], prefix_len, 1, 16, seed=18)
+    q, cache, pt, table, sl = c.dev()
+    plan = B.mla_shared_prefix_get_metadata(sl[:0], prefix_len, 16)
+    out, lse = B.mla_shared_prefix_decode_fwd(q[:0], cache, pt, prefix_len, table[:0], sl[:0],
+                                              *plan)
+    assert out.shape == (0, 1, 16, 512) and lse.shape == (0, 1, 16)
+
+
 def test_wider_indexes_and_strided_inputs():
     c = Case([70, 64, 0], 200, 2, 16, seed=21)
     want = c.run()
