@@ -628,6 +628,31 @@ struct PageSparseWs {
   int width;
 };
 
+// Parts of the decode of `pairs` queries over `pages` pages each.  With a whole number
+// of parts per query no part holds the ends of two of them, each with its own query
+// load and epilogue, and a query with one part has no partials to merge; but the parts
+// left over idle, and the longest part takes a granule rounded up.  So the whole number
+// is taken where its longest part is at most `slack` longer than an equal share of the
+// work, in granules: 5/4, or for one part per query what the lost partials are worth by
+// kernel.  B200, step us with all parts and with the whole number:
+//   128 heads (74 parts), 20 queries x 32 pages 42.5 and 38.9, x 128: 82 and 84; 32 x 32:
+//   55.7 and 50.8; 40 x 16: 53.5 and 37.1, x 32: 66.4 and 61.6, x 64: 90 and 97, x 256:
+//   219 and 277; 60 x 64: 109 and 109
+//   64 heads (148), 32 x 32: 51.9 and 49.3; 50 x 64: 95 and 105; 80 x 16: 70.3 and 59.1,
+//   x 32: 91 and 92, x 256: 375 and 531
+//   16 heads (148), 80 x 8: 37.0 and 34.5, x 16: 47.2 and 51.2, x 256: 298 and 476
+int page_sparse_parts(int pairs, int h_q, int pages, int num_sm_parts) {
+  if (pairs == 0 || pairs > num_sm_parts) return num_sm_parts;
+  const int per_query = num_sm_parts / pairs;
+  const long long granules =
+      mla::granules_of(pages * mla::kPage, mla::plan_params(h_q, pairs).g);
+  const int slack_quarters = per_query > 1 ? 5 : h_q <= 32 ? 12 : h_q <= 64 ? 32 : 16;
+  const long long longest = (granules + per_query - 1) / per_query;
+  const bool whole =
+      (4 * longest - slack_quarters) * num_sm_parts <= 4 * pairs * granules;
+  return whole ? per_query * pairs : num_sm_parts;
+}
+
 PageSparseWs page_sparse_ws_layout(int pairs, int h_q, int d_v, int max_pages, int topk,
                                    int parts) {
   PageSparseWs w{};
@@ -1400,13 +1425,7 @@ int mla_page_sparse_decode(const void* q, const void* kcache, int num_blocks,
   p.taken_table = table;
   p.taken_lens = lens;
   p.pages = pages;
-  // The queries take about as many pages each: with a whole number of parts per
-  // query no part holds the ends of two of them, each with its own query load and
-  // epilogue.  B200, 128 heads, 32 pages, step us with all 74 parts and with the
-  // whole number: 16 queries 38.2 and 36.1, 20: 46.8 and 41.4, 28: 52.3 and 49.1,
-  // 32: 58.6 and 57.3, 40 (16 pages): 50.2 and 41.9; 64 heads, 32 queries, 148
-  // and 128 parts: 56.1 and 54.2.
-  const int parts = pairs <= num_sm_parts ? num_sm_parts / pairs * pairs : num_sm_parts;
+  const int parts = page_sparse_parts(pairs, h_q, w.width, num_sm_parts);
   p.num_parts = parts;
   p.plan = mla::plan_params(h_q, pairs);
   p.metadata = meta;

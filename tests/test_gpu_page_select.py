@@ -275,6 +275,19 @@ def test_long_tables(pages, h_q):
         c.check(c.run(topk), topk)
 
 
+@pytest.mark.parametrize("n,h_q,pages,topk", [(40, 128, 130, 128), (40, 128, 40, 16),
+                                              (76, 64, 130, 120), (76, 64, 20, 8),
+                                              (5, 16, 130, 128), (100, 16, 70, 64)])
+def test_plans_with_and_without_whole_parts_per_query(n, h_q, pages, topk):
+    # sequences that share the pages of one cache
+    c = Case([64 * pages], h_q=h_q, seed=28)
+    g = torch.Generator().manual_seed(28)
+    c.lengths = torch.randint(64 * topk, 64 * pages + 1, (n,), generator=g).tolist()
+    c.table = torch.stack([c.table[0][torch.randperm(pages, generator=g)] for _ in range(n)])
+    c.q = torch.randn((n, 1, h_q, 576), generator=g).to(torch.bfloat16)
+    c.check(c.run(topk), topk)
+
+
 def test_d_v_576():
     c = Case([700, 100], seed=8, d_v=576)
     c.check(c.run(4), 4)
