@@ -125,6 +125,11 @@ def calls():
         lib()
         try:
             from . import _torch_calls
+            from .build import calls_key
+            built_with = getattr(_torch_calls, "BUILT_WITH", "another torch")
+            if built_with != calls_key():
+                raise ImportError(f"_torch_calls was built with {built_with}, this is "
+                                  f"{calls_key()}")
         except ImportError as e:
             raise ImportError(f"{e}: build it with `python -m mla_paged_kv_03_b200.build`") from e
         _calls = _torch_calls

@@ -36,6 +36,13 @@ FLAGS = [
 
 CALLS = os.path.join(HERE, "_torch_calls.so")
 CALLS_DEPS = [os.path.join(CSRC, "torch_calls.cpp"), os.path.join(ROOT, "include", "mla.h")]
+CALLS_BUILT_WITH = os.path.join(HERE, "_torch_calls.built_with")  # calls_key() of CALLS
+
+
+def calls_key() -> str:
+    """The torch and Python whose ABI _torch_calls.so is compiled against."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
 
 
 def _stale(target=LIB, deps=DEPS):
@@ -47,14 +54,18 @@ def _stale(target=LIB, deps=DEPS):
 
 def build_calls(force: bool = False) -> str:
     """Compile _torch_calls.so against the installed torch and libmla_b200.so."""
-    if not force and not _stale(CALLS, CALLS_DEPS):
-        return CALLS
     import torch
+    key = calls_key()
+    if not force and not _stale(CALLS, CALLS_DEPS) and os.path.exists(CALLS_BUILT_WITH):
+        with open(CALLS_BUILT_WITH) as f:
+            if f.read() == key:
+                return CALLS
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
            "-fvisibility=hidden", "-Wall", "-Wno-unknown-pragmas",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DMLA_BUILT_WITH="{key}"',
            "-isystem", os.path.join(base, "include"),
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"),
@@ -65,6 +76,8 @@ def build_calls(force: bool = False) -> str:
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("building _torch_calls.so failed")
+    with open(CALLS_BUILT_WITH, "w") as f:
+        f.write(key)
     return CALLS
 
 

@@ -450,4 +450,8 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, kMeth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__torch_calls() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__torch_calls() {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "BUILT_WITH", MLA_BUILT_WITH) < 0) Py_CLEAR(m);
+  return m;
+}

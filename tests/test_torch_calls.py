@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from mla_paged_kv_03_b200 import binding as B
+from mla_paged_kv_03_b200 import build
 
 BF16 = torch.bfloat16
 
@@ -78,3 +79,24 @@ def test_an_error_of_the_device_is_an_exception():
     r = subprocess.run([sys.executable, "-c", AT_THE_DEVICE], capture_output=True, text=True)
     assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
     assert r.stdout.split().count("raised") == 2
+
+
+def test_a_module_built_with_another_torch_is_built_anew_and_not_used(monkeypatch, tmp_path):
+    assert B.calls().BUILT_WITH == build.calls_key()
+    monkeypatch.setattr(build, "calls_key", lambda: "torch 0.0.0, cpython-00")
+    monkeypatch.setattr(B, "_calls", None)
+    with pytest.raises(ImportError, match="torch 0.0.0"):
+        B.calls()
+    # the build takes the file for stale although it is newer than its sources
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_torch_calls.so"))
+    monkeypatch.setattr(build, "CALLS_BUILT_WITH", str(tmp_path / "_torch_calls.built_with"))
+    for f, text in ((build.CALLS, "old"), (build.CALLS_BUILT_WITH, "torch 1.0, cpython-00")):
+        with open(f, "w") as out:
+            out.write(text)
+    compiled = []
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **kw: compiled.append(cmd) or
+                        build.subprocess.CompletedProcess(cmd, 0, "", ""))
+    build.build_calls()
+    assert len(compiled) == 1 and '-DMLA_BUILT_WITH="torch 0.0.0, cpython-00"' in compiled[0]
+    build.build_calls()
+    assert len(compiled) == 1
