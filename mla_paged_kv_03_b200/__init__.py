@@ -10,7 +10,8 @@ _BINDING_NAMES = (
     "mla_num_sm_parts", "mla_get_metadata", "mla_get_metadata_host", "mla_workspace_size",
     "mla_sparse_workspace_size", "mla_decode_fwd", "mla_fused_norm_rope_attn_rope_cast",
     "mla_sparse_decode", "mla_cache_append", "mla_shared_prefix_get_metadata",
-    "mla_shared_prefix_decode_fwd", "mla_page_keys_update", "mla_page_sparse_decode",
+    "mla_shared_prefix_decode_fwd", "mla_shared_prefix_workspace_size", "mla_page_keys_update",
+    "mla_page_sparse_decode", "mla_page_sparse_workspace_size",
     "device_status", "MLAError", "lib",
 )
 
