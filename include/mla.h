@@ -50,8 +50,9 @@
  *     no work.  mla_last_error() returns a message for the calling thread's
  *     most recent failure.
  *   - An empty row (no visible token) produces O = 0 and LSE = -inf.
- *   - Cache slots that are not visible to a row must still hold finite
- *     values: masked tokens are multiplied by a zero probability.
+ *   - The cache rows of a sequence's tokens must hold finite values, also
+ *     where a query does not see them: masked tokens are multiplied by a zero
+ *     probability.  Rows behind a paged sequence's end may hold anything.
  */
 #ifndef MLA_B200_H_
 #define MLA_B200_H_
@@ -403,11 +404,12 @@ MLA_API int mla_page_sparse_decode(const void* q, const void* kcache, int num_bl
  *                 multiple of 8; a column range of a wider matrix will do).
  *                 d = 576 for 1152- and 656-byte rows, 512 for 528 and 288
  *   slots         int32[n] physical slots (block * 64 + offset); a negative
- *                 one marks a token without a slot (padding): its row is not
- *                 read, nothing is written for it.  A slot >= num_slots is
- *                 skipped too and sets the bad-index status.  The slots
- *                 named must differ: which of two tokens with the same slot
- *                 the row ends up with, or parts of both, is not defined
+ *                 one marks a token without a slot (padding): its row of kv
+ *                 may hold anything (it is read), nothing is written for
+ *                 it.  A slot >= num_slots is skipped too and sets the
+ *                 bad-index status.  The slots named must differ: which of
+ *                 two tokens with the same slot the row ends up with, or
+ *                 parts of both, is not defined
  *   positions     int32[n] for the rotation, or NULL: the last 64 dims are
  *                 stored as they are.  Pairs (2k, 2k+1) of them rotate by
  *                 pos * rope_base^(-2k/64)
@@ -416,13 +418,13 @@ MLA_API int mla_page_sparse_decode(const void* q, const void* kcache, int num_bl
  *                 its RoPE dims: they are normalised, then rotated
  *   kcache        [num_slots] rows of row_bytes bytes, row_bytes one of
  *     1152        576 bf16 (the dense cache)
- *     656         per 128 dims scale = absmax/448 (fp32; 1 for a zero group);
- *                 codes are value * 448 / absmax, with the quotient unrounded
- *                 (value / scale where the scale is below fp32's normal range)
+ *     656         per 128 dims scale = absmax/448 (fp32; 1 for a zero group)
  *     528         per 32 dims scale = the least power of two >= absmax/448
  *     288         per 16 dims scale = e4m3(absmax/6) (1 where that is 0)
  *                 codes are value / scale rounded to the nearest, ties to
- *                 even, saturating; bytes as the sparse decodes read them
+ *                 even, saturating, with absmax/448 unrounded in the 656-byte
+ *                 rows (value * 448 / absmax; as stored below fp32's normal
+ *                 range); bytes as the sparse decodes read them
  *   rows          bf16 [n, d] or NULL: the rows as the cache stands for them,
  *                 bf16(code * scale) (for a prefill over the same tokens);
  *                 rows of tokens without a slot are left as they were

@@ -22,16 +22,18 @@
 // One warp per token: lane l holds the 16-byte units l and l + 32 (8 dims
 // each) of the first 512 dims, and lanes 0..7 the eight units behind them, so
 // that a quantisation group is 16, 4 or 2 neighbouring lanes of one unit index
-// and its maximum takes 4, 2 or 1 shuffles.  A warp keeps its gains in registers and
+// and its maximum takes 4, 2 or 1 shuffles.  The gains lie in shared memory; a warp
 // strides over the tokens.
 //
 // Precision: the norm's sum of squares and 1/sqrt are formed in fp64, y in fp32
 // with the exact products' low parts carried along (one rounding), quotients with
 // one more; with the rounded maximum and scale that is 2^-22 of a quotient.  One
 // that lies within 2^-21 of a rounding border is decided in fp64 from the latent
-// (rotated dims, whose error is relative to their pair: within 2^-18), so that the
-// codes are those of the definition in fp64, but for rotated dims that cancel to
-// less than a 16th of their pair.  (32768 tokens into FP4 rows: 29 us; 24 us
+// (rotated dims, whose error is relative to their pair: within 2^-18), and so are the
+// 528- and 288-byte scales, so that the codes are those of the definition in fp64, but
+// for rotated dims that cancel to less than a 16th of their pair.  A latent without
+// norm needs none of that: its quotients are rounded once, the right way at a border.
+// (32768 tokens with norm into FP4 rows: 27.5 us; 24 us
 // without the second look, where a few codes in a million differ, and 21 us with
 // the squares in fp32 and y = x (g / rms), where some ten do.)
 //

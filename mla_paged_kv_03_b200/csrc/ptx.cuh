@@ -538,14 +538,16 @@ __device__ __forceinline__ void umma_f16_ss_w(uint32_t d_tmem, uint32_t a_lo, ui
       : "memory");
 }
 
-// Instruction descriptor for kind::f16: bf16 x bf16 -> fp32, M x N, with the
-// major-ness of A and B (0 = K-major, 1 = MN-major).
-__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {  // both K-major
+// Instruction descriptor for kind::i8: signed bytes -> int32, M x N, both K-major.
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
   return (2u << 4)                          // D = s32
          | (1u << 7)                        // A = s8
          | (1u << 10)                       // B = s8
          | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
+
+// Instruction descriptor for kind::f16: bf16 x bf16 -> fp32, M x N, with the
+// major-ness of A and B (0 = K-major, 1 = MN-major).
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {
   return (1u << 4)                          // D = fp32
          | (1u << 7)                        // A = bf16
