@@ -173,7 +173,7 @@ static_assert(sizeof(Ctrl) <= cfg::kMiscBytes, "control block too large");
 
 struct Unit {
   int b, lo, hi, split, nsplit;  // shared prefix: b is the unit, not a sequence
-  int L;      // tokens attended: cache_seqlens[b], at most max_pages * 64
+  int L;      // tokens attended: cache_seqlens[b], 0 .. max_pages * 64
   int L_raw;  // cache_seqlens[b] as given (the planner counted its tiles)
 };
 
@@ -215,7 +215,7 @@ struct UnitIter {
       // input fault; of the tiles past it, which are fully masked, a split takes
       // its first if it has no other, so that every split the planner counted
       // still writes its (empty) partial.
-      u.L = L_raw;
+      u.L = max(L_raw, 0);
       if (!prefix && L_raw > P.max_pages * kPage) {
         ptx::set_error(MLA_DEVERR_BAD_INDEX, 0x30);
         u.L = P.max_pages * kPage;

@@ -130,3 +130,19 @@ def test_a_length_past_the_table_does_not_read_block_0(s_q, h_q, d_v, past):
     ro, rl = dense_oracle(case, bt=bt)
     assert_out_close(out, ro)
     assert_lse_close(lse, rl)
+
+
+@pytest.mark.parametrize("s_q,h_q,d_v", DENSE_SHAPES)
+@pytest.mark.parametrize("length", [-1, -64, -1000, -2 ** 31])
+def test_a_negative_length_is_an_empty_sequence(s_q, h_q, d_v, length):
+    case = W.make_dense([640, 130], s_q, h_q, seed=55, d_v=d_v, spare_blocks=2)
+    case.kcache[:] = float("nan")
+    sl = torch.tensor([length, length], dtype=torch.int32)
+    out, lse = dense_gpu(case, sl=sl)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    c = Case([0, 0], 0, s_q, h_q, seed=56)
+    t = list(c.dev())
+    t[1] = torch.full_like(t[1], float("nan"))
+    t[4] = sl.cuda()
+    c.check(c.run(t=t))
