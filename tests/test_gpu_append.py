@@ -324,6 +324,42 @@ def test_codes_of_bf16_values_are_the_definitions(fmt):
     assert torch.equal(got, want), f"{int((got != want).sum())} codes differ"
 
 
+@pytest.mark.parametrize("fmt", ["528", "288"])
+def test_codes_of_rotated_values_without_norm(fmt):
+    """Only the last 64 of the 512 dims are rotated (exceptions as with a norm)."""
+    n, gen = 6000, torch.Generator().manual_seed(43)
+    kv = torch.randn((n, 512), generator=gen).to(torch.bfloat16)
+    positions = torch.randint(0, 1 << 17, (n,), generator=gen, dtype=torch.int32)
+    cache = make_cache(fmt, n // 64 + 1, "cuda", gen)
+    B.mla_cache_append(kv.cuda(), torch.arange(n, dtype=torch.int32, device="cuda"), cache,
+                       positions=positions.cuda())
+    raw = raw_rows(cache)[:n]
+    y, size = expected(kv, positions, None, 0.0, 1e4)
+    per, most = (32, 448.0) if fmt == "528" else (16, 6.0)
+    g = y.reshape(n, 512 // per, per)
+    amax = g.abs().amax(2, keepdim=True)
+    if fmt == "528":
+        scale = torch.exp2(torch.ceil(torch.log2(amax / 448)))
+        assert torch.equal(torch.exp2(raw[:, 512:].double() - 127), scale[..., 0])
+        got = e4m3(raw[:, :512])
+    else:
+        step = torch.exp2(torch.floor(torch.log2((amax / 6).clamp(min=2.0 ** -6))) - 3)
+        scale = torch.round(amax / 6 / step) * step
+        assert torch.equal(e4m3(raw[:, 256:]), scale[..., 0])
+        code = torch.stack([raw[:, :256] & 15, raw[:, :256] >> 4], 2).reshape(n, 512).long()
+        got = E2M1[code & 7] * torch.where(code >= 8, -1.0, 1.0)
+    v = (g / scale).reshape(n, 512)
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    if fmt == "288":
+        step = torch.where(v.abs() < 2, 0.5, torch.where(v.abs() < 4, 1.0, 2.0)).double()
+    want = (torch.round(v / step) * step).clamp(-most, most)
+    steps = v / step
+    unsure = (steps - torch.floor(steps) - 0.5).abs() < 2.0 ** -45 * steps.abs()
+    unsure |= y.abs() < size / 16
+    unsure[:, :448] = False  # exact values
+    assert ((got == want) | unsure).all(), f"{int(((got != want) & ~unsure).sum())} codes differ"
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_append_strided_rows_padding_and_no_rows_output(fmt):
     run(fmt, 77, stride=width(fmt) + 520, pad=(0, 5, 76), seed=4)
