@@ -234,8 +234,8 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
             "contiguous and", index);
     require(n <= std::numeric_limits<int>::max(), "kv has too many rows");
     if (n == 0) return Py_NewRef(a[7]);
-    int64_t stride = kv.stride(0);
-    if (kv.stride(1) != 1 || stride % 8 || (n > 1 && stride < d) ||
+    int64_t stride = n > 1 ? kv.stride(0) : d;
+    if (kv.stride(1) != 1 || stride % 8 || stride < d || stride >= int64_t{1} << 32 ||
         reinterpret_cast<uintptr_t>(kv.data_ptr()) % 16) {
       kv = kv.clone(at::MemoryFormat::Contiguous);
       stride = d;
@@ -258,7 +258,7 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       rows = output(a[7], "rows", {n, d}, at::kBFloat16, kv.device());
     const double eps = number(a[5]), base = number(a[6]);
     launch(index, [&](cudaStream_t stream) {
-      return mla_cache_append(kv.data_ptr(), stride < d ? d : stride, static_cast<int>(d),
+      return mla_cache_append(kv.data_ptr(), stride, static_cast<int>(d),
                               static_cast<const int32_t*>(slots.data_ptr()),
                               positions.defined()
                                   ? static_cast<const int32_t*>(positions.data_ptr())

@@ -367,6 +367,23 @@ def test_append_strided_rows_padding_and_no_rows_output(fmt):
     run(fmt, 65, rows=False, seed=6)
 
 
+@pytest.mark.parametrize("n", [1, 2])
+def test_append_rows_far_apart(n):
+    # the last token of sequences whose hidden states lie 2^32 values apart
+    dev = torch.device("cuda")
+    stride = (1 << 32) + 8
+    wide = torch.empty((n - 1) * stride + 576, dtype=torch.bfloat16, device=dev)
+    kv = wide.as_strided((n, 576), (stride, 1))
+    kv[:] = torch.randn((n, 576), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    cache = torch.zeros((1, 64, 1, 576), dtype=torch.bfloat16, device=dev)
+    B.mla_cache_append(kv, torch.arange(n, dtype=torch.int32, device=dev), cache)
+    assert torch.equal(cache[0, :n, 0], kv) and (cache[0, n:] == 0).all()
+    # (one row's stride does not count, whatever it is)
+    one = wide.as_strided((1, 576), (7, 1))
+    B.mla_cache_append(one, torch.full((1,), 9, dtype=torch.int32, device=dev), cache)
+    assert torch.equal(cache[0, 9, 0], one[0])
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_append_a_cache_past_2_gib(fmt):
     # slots whose byte offsets pass 32 bits
